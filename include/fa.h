@@ -210,6 +210,80 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
                           fa_kv_format v_format, void* workspace, size_t workspace_bytes,
                           fa_stream_t stream);
 
+/* Ragged batches over page pools: the three calls that a serving step makes beside
+ * fa_decode_paged -- write the new tokens into the pages, attend from them, and take tokens back
+ * out of the pages -- for the batched server session of "perf(rocm): defer SDPA accumulator
+ * rescale, stage Q once per block (#2306)" (Conversation) over the cache that "FlashAttention on
+ * gfx90a: Why It's Broken and How to Fix It" (Impact of the V Dequant Patch) keeps in q4_0.
+ *
+ * What they share:
+ *  packed rows : tensors [rows, heads, D] in `dtype`, innermost contiguous; row and head strides in
+ *                elements, multiples of 8 and not negative (a tensor cut out of a fused projection,
+ *                or head-major rows, need no copy).  Every base pointer 16-byte aligned.  No two
+ *                (row, head) of a tensor overlap (new keys and values, which are only read, may:
+ *                a stride of 0 broadcasts).
+ *  row_starts  : device int32 [B + 1]: sequence b owns rows row_starts[b] .. row_starts[b + 1] - 1,
+ *                n_b >= 0 of them.  Rising from row_starts[0] >= 0 to row_starts[B] <= rows; rows
+ *                outside (padding up to a fixed batch size) are neither read nor written.
+ *  seq_lens    : device int32 [B], 0 <= seq_lens[b] <= pages_per_seq * page_size: tokens of the
+ *                sequence with its rows included.  The rows are its last tokens: row row_starts[b]
+ *                + i is position seq_lens[b] - n_b + i.
+ *  block_table : device int32 [B, pages_per_seq], as in fa_decode_paged; entries past a sequence's
+ *                last page are not read
+ *  k_pages,
+ *  v_pages     : page pools [num_pages, Hkv, page_size, D], each dense (`dtype`) or a q4_0 tensor
+ *                built for that shape (fa_q4_0_bytes(num_pages, Hkv, page_size, D))
+ *  rows == 0 returns FA_OK without a launch.  The batch is read on the device, so a captured call
+ *  serves other batches of the same B and rows when the three arrays are rewritten.  Found on the
+ *  device: row_starts out of order or out of range (the call then writes nothing), a page number or
+ *  length out of range, a position below 0 (fa_append_paged and fa_read_paged skip that row); each
+ *  is recorded and fa_get_status then returns FA_ERR_INVALID_ARG.
+ *
+ * fa_append_paged writes every row of k_new (and v_new) [rows, Hkv, D] to its position's page, slot
+ * position % page_size: q4_0 pools get the bits fa_quantize_q4_0 would produce (inputs finite),
+ * dense pools a copy.  v_new and v_pages may both be NULL.  Every other token of the pools is left
+ * as it was.  Rows of different sequences must not share a slot.  Any page_size; D a multiple of 32.
+ *
+ * fa_read_paged is its inverse: k_out (and v_out) [rows, Hkv, D] get the values that the rows'
+ * positions hold, q4_0 ones as (nibble - 8) * scale rounded once to `dtype`.  With n_b =
+ * seq_lens[b] it takes out whole sequences.  Same limits. */
+fa_status fa_append_paged(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                          const int32_t* block_table, const int32_t* row_starts,
+                          const int32_t* seq_lens, int B, int rows, int Hkv, int D, int num_pages,
+                          int page_size, int pages_per_seq, int64_t k_row_stride,
+                          int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                          fa_dtype dtype, fa_kv_format k_format, fa_kv_format v_format,
+                          fa_stream_t stream);
+fa_status fa_read_paged(const void* k_pages, const void* v_pages, void* k_out, void* v_out,
+                        const int32_t* block_table, const int32_t* row_starts,
+                        const int32_t* seq_lens, int B, int rows, int Hkv, int D, int num_pages,
+                        int page_size, int pages_per_seq, int64_t k_row_stride,
+                        int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                        fa_dtype dtype, fa_kv_format k_format, fa_kv_format v_format,
+                        fa_stream_t stream);
+
+/* Attention of a ragged batch of new tokens over page pools (see above for the batch): for every row
+ * t of sequence b and query head h, the softmax over the sequence's keys in the pages up to the row's
+ * own position (causal != 0) or over all seq_lens[b] of them (causal == 0).  The rows' own keys and
+ * values are in the pages already (fa_append_paged).  Sequences with one new token, with a chunk of a
+ * prompt and with none mix freely in a call.
+ *  q, o      : packed rows [rows, Hq, D]; a row that sees no key (a position below 0, or an empty
+ *              sequence) gives zeros; o may not overlap q
+ *  D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, page_size a multiple of 16.
+ *  A tile of a page outside the pool reads as zeros (recorded, see above).  What the pools hold past
+ *  a sequence's end does not matter, NaN included.
+ *  workspace : >= fa_prefill_paged_workspace_bytes(Hq, Hkv, D) bytes on the current device, contents
+ *              on entry irrelevant, not shared by calls in flight at the same time (see fa_fwd_ex) */
+size_t fa_prefill_paged_workspace_bytes(int Hq, int Hkv, int D);
+fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
+                           const int32_t* block_table, const int32_t* row_starts,
+                           const int32_t* seq_lens, int B, int rows, int Hq, int Hkv, int D,
+                           int num_pages, int page_size, int pages_per_seq, int64_t q_row_stride,
+                           int64_t q_head_stride, int64_t o_row_stride, int64_t o_head_stride,
+                           int causal, float scale, fa_dtype dtype, fa_kv_format k_format,
+                           fa_kv_format v_format, void* workspace, size_t workspace_bytes,
+                           fa_stream_t stream);
+
 /* The explicit (non-flash) attention path, for comparison with fa_fwd_kv: q4_0 sides are first
  * expanded to dense f16/bf16, S = scale * Q K^T is written out in f32 by a batched GEMM, a
  * softmax kernel makes P (causal mask, rounded to the dtype), and O = P V is a second batched
@@ -289,7 +363,8 @@ fa_status fa_prefill_append_q4_0(const void* q, const void* k_new, const void* v
 /* Synchronize `stream`, then report (and clear) any device-side error recorded by this
  * library's kernels since the last call: FA_ERR_TIMEOUT when a bounded wait inside a kernel ran
  * out (the kernel then abandoned its work and returned), FA_ERR_INVALID_ARG when a device-side
- * index input was out of range (fa_decode_paged), FA_ERR_UNSUPPORTED when a prefill CTA's
+ * index input was out of range (fa_decode_paged, fa_append_paged, fa_read_paged,
+ * fa_prefill_paged), FA_ERR_UNSUPPORTED when a prefill CTA's
  * share of the work did not fit its segment table (see fa_prefill_schedule; the launch plans
  * never produce one), FA_ERR_CUDA when the stream reports a CUDA error, FA_OK otherwise. */
 fa_status fa_get_status(fa_stream_t stream);

@@ -9,6 +9,7 @@ if it is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import functools
@@ -30,6 +31,7 @@ EXPORTED = (
     "fa_decode_paged_workspace_bytes", "fa_fwd_explicit", "fa_explicit_workspace_bytes",
     "fa_prefill_schedule", "fa_decode_schedule", "fa_fwd_kv_stats",
     "fa_prefill_append_workspace_bytes", "fa_prefill_append_q4_0",
+    "fa_append_paged", "fa_read_paged", "fa_prefill_paged", "fa_prefill_paged_workspace_bytes",
 )
 
 _lib = None
@@ -110,6 +112,15 @@ def load_from(p: str) -> ctypes.CDLL:
     lib.fa_fwd_explicit.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, i, vp, sz,
                                     vp]
     lib.fa_fwd_explicit.restype = i
+    i64 = ctypes.c_int64
+    lib.fa_append_paged.argtypes = [vp] * 7 + [i] * 7 + [i64] * 4 + [i, i, i, vp]
+    lib.fa_append_paged.restype = i
+    lib.fa_read_paged.argtypes = [vp] * 7 + [i] * 7 + [i64] * 4 + [i, i, i, vp]
+    lib.fa_read_paged.restype = i
+    lib.fa_prefill_paged_workspace_bytes.argtypes = [i] * 3
+    lib.fa_prefill_paged_workspace_bytes.restype = sz
+    lib.fa_prefill_paged.argtypes = [vp] * 7 + [i] * 8 + [i64] * 4 + [i, f, i, i, i, vp, sz, vp]
+    lib.fa_prefill_paged.restype = i
     return lib
 
 
@@ -130,6 +141,16 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _allocating_on(stream):
+    """Context in which torch allocates (and fills) on `stream`, the stream of the launch: what a call
+    allocates for itself must not be reused, or still be being filled, beside it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _dtype_code(t: torch.dtype) -> int:
@@ -582,6 +603,132 @@ def fa_decode_paged(q, k_pages, v_pages, block_table: torch.Tensor, seq_lens: to
                                page, pps, float(scale), _dtype_code(q.dtype), kf, vf,
                                workspace.data_ptr(), workspace.numel(), _stream(stream)),
            "fa_decode_paged")
+    return o
+
+
+def _paged_batch(block_table, row_starts, seq_lens):
+    """(B, pages_per_seq) of a ragged batch's device arrays (see fa.h, packed rows)."""
+    for name, t, dim in (("block_table", block_table, 2), ("row_starts", row_starts, 1),
+                         ("seq_lens", seq_lens, 1)):
+        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
+    B, pps = block_table.shape
+    if seq_lens.shape[0] != B or row_starts.shape[0] != B + 1:
+        raise ValueError("block_table [B, pages_per_seq], row_starts [B + 1] and seq_lens [B] must "
+                         "describe the same B sequences")
+    return B, pps
+
+
+def _packed(t, what, dtype, heads, D, rows):
+    """(pointer, row stride, head stride) of packed rows [rows, heads, D] with contiguous
+    innermost; strides of dimensions of one entry are not used and passed as D."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if tuple(t.shape) != (rows, heads, D) or (t.stride(2) != 1 and D > 1):
+        raise ValueError(f"{what} must be a [{rows}, {heads}, {D}] tensor with contiguous "
+                         "innermost dimension")
+    return (t.data_ptr(), t.stride(0) if rows > 1 else D, t.stride(1) if heads > 1 else D)
+
+
+def _paged_pools(k_pages, v_pages, dtype):
+    kf, shape = _side(k_pages)
+    vf = kf
+    if v_pages is not None:
+        vf, vshape = _side(v_pages)
+        if vshape != shape:
+            raise ValueError("k_pages and v_pages must have the same [num_pages, Hkv, page_size, "
+                             "D]")
+    for t, fmt in ((k_pages, kf), (v_pages, vf)):
+        if t is not None and fmt == FA_KV_DENSE and t.dtype != dtype:
+            raise TypeError(f"dense pools must be {dtype}, as the packed rows are")
+    return kf, vf, shape
+
+
+def _paged_rows(fn, k, v, k_pages, v_pages, block_table, row_starts, seq_lens, stream):
+    """The arguments that fa_append_paged and fa_read_paged share, checked and passed on."""
+    if (v is None) != (v_pages is None):
+        raise ValueError("give both V rows and v_pages, or neither")
+    if k.dim() != 3:
+        raise ValueError("packed rows must be [rows, Hkv, D]")
+    rows = k.shape[0]
+    kf, vf, (NP, Hkv, page, D) = _paged_pools(k_pages, v_pages, k.dtype)
+    B, pps = _paged_batch(block_table, row_starts, seq_lens)
+    kp, krs, khs = _packed(k, "K rows", k.dtype, Hkv, D, rows)
+    vp, vrs, vhs = (None, D, D) if v is None else _packed(v, "V rows", k.dtype, Hkv, D, rows)
+    dt = _dtype_code(k.dtype)
+    _on_device(k, v, k_pages, v_pages, block_table, row_starts, seq_lens)
+    pages = (k_pages.data_ptr(), v_pages.data_ptr() if v_pages is not None else None)
+    ptrs = (kp, vp, *pages) if fn == "fa_append_paged" else (*pages, kp, vp)
+    _check(getattr(load(), fn)(*ptrs, block_table.data_ptr(), row_starts.data_ptr(),
+                               seq_lens.data_ptr(), B, rows, Hkv, D, NP, page, pps, krs, khs, vrs,
+                               vhs, dt, kf, vf, _stream(stream)), fn)
+
+
+def fa_append_paged(k_new: torch.Tensor, v_new: torch.Tensor | None, k_pages, v_pages,
+                    block_table: torch.Tensor, row_starts: torch.Tensor, seq_lens: torch.Tensor,
+                    *, stream=None) -> None:
+    """Write a ragged batch's new keys and values into page pools.  k_new, v_new [rows, Hkv, D]
+    packed rows (any row and head strides that are multiples of 8); k_pages, v_pages [num_pages,
+    Hkv, page_size, D], each dense or a Q4Tensor; block_table [B, pages_per_seq], row_starts [B + 1]
+    and seq_lens [B] (lengths with the new tokens) int32 on the device.  v_new and v_pages may both
+    be None."""
+    _paged_rows("fa_append_paged", k_new, v_new, k_pages, v_pages, block_table, row_starts,
+                seq_lens, stream)
+
+
+def fa_read_paged(k_pages, v_pages, block_table: torch.Tensor, row_starts: torch.Tensor,
+                  seq_lens: torch.Tensor, k_out: torch.Tensor,
+                  v_out: torch.Tensor | None = None, *, stream=None):
+    """The inverse of fa_append_paged: the last row_starts[b + 1] - row_starts[b] tokens of every
+    sequence, read out of the pages into packed rows k_out, v_out [rows, Hkv, D] (q4_0 pools
+    dequantized).  Returns (k_out, v_out)."""
+    _paged_rows("fa_read_paged", k_out, v_out, k_pages, v_pages, block_table, row_starts, seq_lens,
+                stream)
+    return k_out, v_out
+
+
+def fa_prefill_paged_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return int(load().fa_prefill_paged_workspace_bytes(int(Hq), int(Hkv), int(D)))
+
+
+def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tensor,
+                     row_starts: torch.Tensor, seq_lens: torch.Tensor,
+                     o: torch.Tensor | None = None, *, causal: bool = True,
+                     scale: float | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of a ragged batch of new tokens over page pools (the rows' own keys and values
+    already in them, see fa_append_paged).  q, o [rows, Hq, D] packed rows; the batch and the pools
+    as for fa_append_paged.  Rows that belong to no sequence are left as they are in o (zeros where
+    o is allocated here)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, D]")
+    if v_pages is None:
+        raise ValueError("fa_prefill_paged needs both pools")
+    rows, Hq, D = q.shape
+    kf, vf, (NP, Hkv, page, Dk) = _paged_pools(k_pages, v_pages, q.dtype)
+    if Dk != D:
+        raise ValueError("head dim of the pools does not match q")
+    B, pps = _paged_batch(block_table, row_starts, seq_lens)
+    if o is None:
+        with _allocating_on(stream):
+            o = torch.zeros((rows, Hq, D), dtype=q.dtype, device=q.device)
+    qp, qrs, qhs = _packed(q, "q", q.dtype, Hq, D, rows)
+    op, ors, ohs = _packed(o, "o", q.dtype, Hq, D, rows)
+    dt = _dtype_code(q.dtype)
+    _on_device(q, k_pages, v_pages, o, block_table, row_starts, seq_lens, workspace)
+    lib = load()
+    if workspace is None:
+        with _allocating_on(stream):
+            workspace = torch.empty(max(lib.fa_prefill_paged_workspace_bytes(Hq, Hkv, D), 16),
+                                    dtype=torch.uint8, device=q.device)
+    if scale is None:
+        scale = D ** -0.5
+    _check(lib.fa_prefill_paged(qp, k_pages.data_ptr(), v_pages.data_ptr(), op,
+                                block_table.data_ptr(), row_starts.data_ptr(), seq_lens.data_ptr(),
+                                B, rows, Hq, Hkv, D, NP, page, pps, qrs, qhs, ors, ohs,
+                                int(bool(causal)), float(scale), dt, kf, vf, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream)),
+           "fa_prefill_paged")
     return o
 
 

@@ -1,6 +1,7 @@
 // C-ABI front end: argument checks, TMA descriptors, kernel dispatch, device status.
 #include <math.h>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/fa.h"
@@ -49,18 +50,27 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D tiled map over a contiguous [d2][d1][d0] tensor; box = {box0, box1, 1}.
-bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t d0,
-              uint64_t d1, uint64_t d2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw) {
+// 3-D tiled map over a [d2][d1][d0] tensor with contiguous innermost rows; s1, s2: byte strides of
+// d1 and d2
+bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t d0,
+                      uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t box0,
+                      uint32_t box1, uint32_t box2, CUtensorMapSwizzle sw) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {d0 * esize, d0 * d1 * esize};
-  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint64_t strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {box0, box1, box2};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// the same over a contiguous tensor of esize-byte elements; box = {box0, box1, 1}
+bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t d0,
+              uint64_t d1, uint64_t d2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw) {
+  return make_map_strided(m, base, dt, d0, d1, d2, d0 * esize, d0 * d1 * esize, box0, box1, 1,
+                          sw);
 }
 
 // map of a K or V tensor [BHkv][Scap][D]: q4_0 nibble tiles (D/2 bytes x `tile` keys, 64-B or
@@ -503,6 +513,191 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
                                                                                  : FA_ERR_CUDA;
 }
 
+// checks that the paged operators share: the batch, the pools and one side's formats
+static fa_status check_paged(const void* k_pages, const int32_t* block_table,
+                             const int32_t* row_starts, const int32_t* seq_lens, int B, int rows,
+                             int Hkv, int D, int num_pages, int page_size, int pages_per_seq,
+                             int dtype, int k_format, int v_format) {
+  if (!aligned16(k_pages)) return FA_ERR_INVALID_ARG;
+  for (const int32_t* p : {block_table, row_starts, seq_lens})
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return FA_ERR_INVALID_ARG;
+  if (B < 1 || rows < 0 || Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1 ||
+      pages_per_seq < 1)
+    return FA_ERR_INVALID_ARG;
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+  if ((k_format != FA_KV_DENSE && k_format != FA_KV_Q4_0) ||
+      (v_format != FA_KV_DENSE && v_format != FA_KV_Q4_0))
+    return FA_ERR_INVALID_ARG;
+  if (B > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+  if (D % 32 || D > 65536) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(page_size) * pages_per_seq > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * Hkv >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  // offsets are 64-bit; keep every tensor far below the address-space limits (the first bound
+  // keeps the second product within 64 bits)
+  if (static_cast<int64_t>(num_pages) * Hkv * page_size >= (1LL << 40) ||
+      static_cast<int64_t>(num_pages) * Hkv * page_size * D >= (1LL << 40) ||
+      static_cast<int64_t>(rows) * Hkv * D >= (1LL << 40))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// packed rows [rows][heads][D] with element strides: 16-byte aligned, strides multiples of 8
+// elements, the whole far below the address-space limits.  apart: also no two (row, head) overlap,
+// rows inside heads or heads inside rows.
+static bool packed_ok(const void* x, int rows, int heads, int D, int64_t row_stride,
+                      int64_t head_stride, bool apart) {
+  constexpr int64_t kMax = 1LL << 40;
+  if (!aligned16(x) || row_stride < 0 || head_stride < 0 || row_stride % 8 || head_stride % 8 ||
+      row_stride > kMax / rows || head_stride > kMax / heads)
+    return false;
+  if (!apart) return true;
+  const bool many_rows = rows > 1, many_heads = heads > 1;
+  if ((many_rows && row_stride < D) || (many_heads && head_stride < D)) return false;
+  return !many_rows || !many_heads || row_stride >= (heads - 1) * head_stride + D ||
+         head_stride >= (rows - 1) * row_stride + D;
+}
+
+static PagedSide paged_side(const void* x, int64_t row_stride, int64_t head_stride,
+                            const void* pages, bool q4, int64_t pool_rows, int D) {
+  uint8_t* p = static_cast<uint8_t*>(const_cast<void*>(pages));
+  PagedSide s;
+  s.x = const_cast<void*>(x);
+  s.row_stride = row_stride;
+  s.head_stride = head_stride;
+  s.pages = p;
+  s.scale = q4 ? p + q4_scale_offset(pool_rows, D) : nullptr;
+  s.q4 = q4;
+  return s;
+}
+
+static fa_status paged_rows(bool append, const void* k_rows, const void* v_rows,
+                            const void* k_pages, const void* v_pages, const int32_t* block_table,
+                            const int32_t* row_starts, const int32_t* seq_lens, int B, int rows,
+                            int Hkv, int D, int num_pages, int page_size, int pages_per_seq,
+                            int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                            int64_t v_head_stride, int dtype, int k_format, int v_format,
+                            fa_stream_t stream) {
+  const fa_status st = check_paged(k_pages, block_table, row_starts, seq_lens, B, rows, Hkv, D,
+                                   num_pages, page_size, pages_per_seq, dtype, k_format, v_format);
+  if (st != FA_OK || rows == 0) return st;
+  if ((v_rows == nullptr) != (v_pages == nullptr)) return FA_ERR_INVALID_ARG;
+  if (v_pages && !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
+  if (!packed_ok(k_rows, rows, Hkv, D, k_row_stride, k_head_stride, !append))
+    return FA_ERR_INVALID_ARG;
+  if (v_rows && !packed_ok(v_rows, rows, Hkv, D, v_row_stride, v_head_stride, !append))
+    return FA_ERR_INVALID_ARG;
+  const int64_t pool_rows = static_cast<int64_t>(num_pages) * Hkv * page_size;
+  const PagedBatch batch = {block_table, row_starts, seq_lens,  B,
+                            rows,        num_pages,  page_size, pages_per_seq};
+  const cudaError_t e = paged_rows_launch(
+      append, batch,
+      paged_side(k_rows, k_row_stride, k_head_stride, k_pages, k_format == FA_KV_Q4_0, pool_rows,
+                 D),
+      paged_side(v_rows, v_row_stride, v_head_stride, v_pages, v_format == FA_KV_Q4_0, pool_rows,
+                 D),
+      Hkv, D, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_append_paged(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                          const int32_t* block_table, const int32_t* row_starts,
+                          const int32_t* seq_lens, int B, int rows, int Hkv, int D, int num_pages,
+                          int page_size, int pages_per_seq, int64_t k_row_stride,
+                          int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                          fa_dtype dtype, fa_kv_format k_format, fa_kv_format v_format,
+                          fa_stream_t stream) {
+  return paged_rows(true, k_new, v_new, k_pages, v_pages, block_table, row_starts, seq_lens, B,
+                    rows, Hkv, D, num_pages, page_size, pages_per_seq, k_row_stride,
+                    k_head_stride, v_row_stride, v_head_stride, dtype, k_format, v_format,
+                    stream);
+}
+
+fa_status fa_read_paged(const void* k_pages, const void* v_pages, void* k_out, void* v_out,
+                        const int32_t* block_table, const int32_t* row_starts,
+                        const int32_t* seq_lens, int B, int rows, int Hkv, int D, int num_pages,
+                        int page_size, int pages_per_seq, int64_t k_row_stride,
+                        int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                        fa_dtype dtype, fa_kv_format k_format, fa_kv_format v_format,
+                        fa_stream_t stream) {
+  return paged_rows(false, k_out, v_out, k_pages, v_pages, block_table, row_starts, seq_lens, B,
+                    rows, Hkv, D, num_pages, page_size, pages_per_seq, k_row_stride,
+                    k_head_stride, v_row_stride, v_head_stride, dtype, k_format, v_format,
+                    stream);
+}
+
+size_t fa_prefill_paged_workspace_bytes(int Hq, int Hkv, int D) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128)) return 0;
+  return paged_prefill_workspace(D, num_sms());
+}
+
+fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
+                           const int32_t* block_table, const int32_t* row_starts,
+                           const int32_t* seq_lens, int B, int rows, int Hq, int Hkv, int D,
+                           int num_pages, int page_size, int pages_per_seq, int64_t q_row_stride,
+                           int64_t q_head_stride, int64_t o_row_stride, int64_t o_head_stride,
+                           int causal, float scale, fa_dtype dtype, fa_kv_format k_format,
+                           fa_kv_format v_format, void* workspace, size_t workspace_bytes,
+                           fa_stream_t stream) {
+  fa_status st = check_paged(k_pages, block_table, row_starts, seq_lens, B, rows, Hkv, D,
+                             num_pages, page_size, pages_per_seq, dtype, k_format, v_format);
+  if (st != FA_OK) return st;
+  if (!aligned16(v_pages) || Hq < 1 || Hq % Hkv) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (rows > 0 && (!packed_ok(q, rows, Hq, D, q_row_stride, q_head_stride, true) ||
+                   !packed_ok(o, rows, Hq, D, o_row_stride, o_head_stride, true)))
+    return FA_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (G > 128 || page_size % 16) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(rows) * Hq * D >= (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  const int nsm = num_sms();
+  const size_t need = paged_prefill_workspace(D, nsm);
+  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))
+    return FA_ERR_INVALID_ARG;
+  if (rows == 0) return FA_OK;
+  if (nsm < 1) return FA_ERR_CUDA;
+  const bool bf16 = dtype == FA_BF16;
+  const bool kq4 = k_format == FA_KV_Q4_0;
+  const bool vq4 = v_format == FA_KV_Q4_0;
+  const CUtensorMapDataType tdt =
+      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle nib_sw =
+      D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  const uint64_t blocks = static_cast<uint64_t>(num_pages) * Hkv;  // (page, kv head) blocks
+  const uint32_t box = static_cast<uint32_t>(paged_prefill_box(page_size));
+  const size_t scale_off = q4_scale_offset(static_cast<int64_t>(blocks) * page_size, D);
+  PagedPrefillLaunch L;
+  // a dimension of one row or head is never stepped along: any valid stride will do
+  const uint64_t qh = 2 * static_cast<uint64_t>(Hq > 1 ? q_head_stride : D);
+  const uint64_t qr = 2 * static_cast<uint64_t>(rows > 1 ? q_row_stride : D);
+  if (!make_map_strided(&L.tm_q, q, tdt, D, Hq, rows, qh, qr, 64, G, 128 / G,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !kv_map(&L.tm_k, k_pages, kq4, tdt, D, page_size, blocks, box, nib_sw) ||
+      !kv_map(&L.tm_v, v_pages, vq4, tdt, D, page_size, blocks, box, nib_sw))
+    return FA_ERR_CUDA;
+  L.batch = PagedBatch{block_table, row_starts, seq_lens,  B,
+                       rows,        num_pages,  page_size, pages_per_seq};
+  L.o = o;
+  L.o_row_stride = o_row_stride;
+  L.o_head_stride = o_head_stride;
+  L.k_scale = kq4 ? static_cast<const uint8_t*>(k_pages) + scale_off : nullptr;
+  L.v_scale = vq4 ? static_cast<const uint8_t*>(v_pages) + scale_off : nullptr;
+  L.Hq = Hq;
+  L.Hkv = Hkv;
+  L.D = D;
+  L.causal = causal ? 1 : 0;
+  L.scale = scale;
+  L.bf16 = bf16;
+  L.kq4 = kq4;
+  L.vq4 = vq4;
+  L.workspace = workspace;
+  L.tag = next_call_tag();
+  L.num_sms = nsm;
+  return paged_prefill_launch(L, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
 size_t fa_explicit_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D,
                                    fa_kv_format k_format, fa_kv_format v_format) {
   if (check_common(B, Hq, Hkv, Sq, Sk, D, 0, 0, 1.f, FA_F16, k_format) != FA_OK) return 0;
@@ -583,15 +778,19 @@ fa_status fa_get_status(fa_stream_t stream) {
   const uint32_t a = prefill_take_error();
   const uint32_t b = decode_take_error();
   const uint32_t x = explicit_take_error();
+  const uint32_t r = paged_take_error();
+  const uint32_t p = paged_prefill_take_error();
   uint32_t c = 0;
   if (cudaMemcpyFromSymbol(&c, g_debug_error, sizeof(c)) != cudaSuccess) return FA_ERR_CUDA;
   const uint32_t z = 0;
   if (c != 0 && cudaMemcpyToSymbol(g_debug_error, &z, sizeof(z)) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (a == 0xffffffffu || b == 0xffffffffu || x == 0xffffffffu) return FA_ERR_CUDA;
-  if (b == kErrBadIndex) return FA_ERR_INVALID_ARG;
+  if (a == 0xffffffffu || b == 0xffffffffu || x == 0xffffffffu || r == 0xffffffffu ||
+      p == 0xffffffffu)
+    return FA_ERR_CUDA;
+  if (b == kErrBadIndex || r == kErrBadIndex || p == kErrBadIndex) return FA_ERR_INVALID_ARG;
   if (a == kErrSchedule) return FA_ERR_UNSUPPORTED;
-  if (a || b || c || x) return FA_ERR_TIMEOUT;
+  if (a || b || c || x || p) return FA_ERR_TIMEOUT;
   return FA_OK;
 }
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fa_paged.cuh"
+
 namespace fa {
 
 // 3-D tiled TMA map over a contiguous [d2][d1][d0] tensor of esize-byte elements; box =
@@ -111,6 +113,42 @@ struct QuantJob {
 };
 cudaError_t quantize_launch(QuantJob j0, QuantJob j1, int64_t BH, int S_src, int Scap, int pos0,
                             int D, bool bf16, cudaStream_t stream);
+
+// Rows moved between packed tensors and page pools, K and (x != nullptr) V in one launch.  x: packed
+// rows [rows][Hkv][D] with strides in elements; pages: a dense pool or a q4_0 pool's nibble plane
+// with scale, its scale plane.
+struct PagedSide {
+  void* x;
+  int64_t row_stride, head_stride;
+  void* pages;
+  void* scale;
+  bool q4;
+};
+cudaError_t paged_rows_launch(bool append, const PagedBatch& b, const PagedSide& k,
+                              const PagedSide& v, int Hkv, int D, bool bf16,
+                              cudaStream_t stream);
+uint32_t paged_take_error();
+
+// ragged prefill over page pools (fa_prefill_paged)
+struct PagedPrefillLaunch {
+  CUtensorMap tm_q, tm_k, tm_v;  // Q tiles {64, G, tokens}; page boxes of K and V (kv_box rows)
+  PagedBatch batch;
+  void* o;
+  int64_t o_row_stride, o_head_stride;
+  const void* k_scale;
+  const void* v_scale;
+  int Hq, Hkv, D, causal;
+  float scale;
+  bool bf16, kq4, vq4;
+  void* workspace;
+  uint32_t tag;
+  int num_sms;
+};
+cudaError_t paged_prefill_launch(const PagedPrefillLaunch& L, cudaStream_t stream);
+size_t paged_prefill_workspace(int D, int num_sms);
+// rows of a K or V box: the part of a page that a 128-key tile takes with one copy
+int paged_prefill_box(int page_size);
+uint32_t paged_prefill_take_error();
 
 // the explicit (non-flash) path: dequant (q4_0 sides), S = scale Q K^T (f32), softmax -> P,
 // O = P V; workspace = S, P and the dequantized K / V

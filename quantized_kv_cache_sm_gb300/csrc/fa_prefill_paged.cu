@@ -1,0 +1,1058 @@
+// Causal attention of a ragged batch of new tokens over page pools (fa_prefill_paged), sm_103a; K
+// and V each dense or q4_0.
+//
+// What it computes: for row t of sequence b (position p = lens[b] - n_b + its place in the
+// sequence's rows) and query head h
+//     O[t, h] = sum_{j <= p} softmax_j(scale <Q[t, h], K[b, g, j]>) V[b, g, j],  g = h / (Hq / Hkv),
+// K[b, g, j] being the pool row that the block table gives for position j; causal = 0 lets every row
+// see all lens[b] keys, and a row that sees no key gives zeros.  The chunked-prefill call and the
+// deferred rescale are those of "perf(rocm): defer SDPA accumulator rescale, stage Q once per block
+// (#2306)" (Conversation; What changed) as fa_prefill.cu builds them; the softmax, dequant and tile
+// layout are the same code (fa_prefill_tile.cuh).
+//
+//  * A 128-row query tile holds all G = Hq / Hkv query heads of floor(128 / G) consecutive tokens:
+//    one TMA box {64, G, tokens} of Q, rows in token-major order.  A K/V tile is then read once for
+//    the whole group, and a few new tokens fill G times as many rows as they would head by head.
+//  * A work unit is a pair of consecutive tiles (A, B) of one sequence and kv head; its steps are
+//    the 128-key blocks that the pair sees, at least one.  All units' steps are concatenated
+//    (sequence, then pair, then kv head) and cut evenly over one CTA per SM, whatever the mix of
+//    long chunks and single tokens; a unit cut between CTAs is merged by the piece that finds all
+//    its siblings published.  Lengths live on the device, so every CTA finds its own run: one warp
+//    sums the steps of the batch, locates the run and feeds the other roles one segment (a run of
+//    steps of one unit) at a time through a small queue in shared memory.
+//  * A 128-key tile is fetched as 128 / box boxes of box = gcd(page_size, 128) keys, each with its
+//    own page.  Boxes that hold no key of the sequence are fetched from outside the pool, which TMA
+//    fills with zeros without reading memory; the rows of a dense V tile between the sequence's end
+//    and its box's are cleared in shared memory, so that what an unused slot holds (NaN included)
+//    never meets a zero weight.  q4_0 rows past the end get a zero scale.
+//
+// Warp roles: as in fa_prefill.cu (0 producer and scheduler, 1 TMEM and MMA issuer, 2-3 and 12-15
+// q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B).
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "fa_paged.cuh"
+#include "fa_prefill_tile.cuh"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+__device__ uint32_t g_prefill_paged_error;
+
+namespace {
+
+// barrier slots (8 bytes each) inside the barrier area
+enum {
+  pbQFull = 0,
+  pbSFull = 1,       // + tile (2)
+  pbPReady = 3,      // + tile (2)
+  pbODone = 5,       // + tile (2): after the tile's last PV MMA of a segment
+  pbDrain = 7,
+  pbRingFull = 8,    // + stage (up to 8)
+  pbRingEmpty = 16,  // + stage
+  pbRawFull = 24,    // + raw stage (up to 4)
+  pbRawEmpty = 28,   // + raw stage
+  pbQEmpty = 32,     // the segment's last QK MMA has read the Q tiles
+  pbOFree = 33,      // + tile (2): the segment's epilogue has read O out of TMEM
+  pbPiece = 35,      // all 256 softmax threads have stored their rows of a piece
+  pbDecided = 36,    // the piece's flag is published and the merge decision made
+  pbTail = 37,       // a V tile that needs rows cleared has landed
+  pbSegFull = 38,    // + queue slot (kSegQ)
+  pbSegEmpty = 42,   // + queue slot
+  pbCount = 46
+};
+constexpr int kSegQ = 4;
+constexpr int kOffTmem = pbCount * 8;
+constexpr int kOffAbort = kOffTmem + 8;
+constexpr int kOffMerge = kOffAbort + 8;
+constexpr int kOffPlan = kOffMerge + 8;  // int64: steps in all, this CTA's first and end step
+constexpr int kOffSegQ = 512;            // the segment queue
+
+// one segment: steps [j0, j1) of a unit
+struct PSeg {
+  int row0;       // packed row of tile A's first token
+  int g;          // kv head
+  int tokA, tokB; // tokens of the tiles (0: tile absent)
+  int pos0;       // position of tile A's first token
+  int len;        // keys of the sequence
+  int nbA, nbB, nb;  // key blocks of the tiles and of the unit
+  int j0, j1;     // j1 = -1: no more segments
+  int64_t unit_start;  // global step of the unit's block 0
+};
+static_assert(sizeof(PSeg) <= 64 && kOffSegQ + kSegQ * 64 <= 512 + 1024, "segment queue");
+
+struct PArgs {
+  PagedBatch batch;
+  uint8_t* o;
+  int64_t o_row_stride, o_head_stride;  // bytes
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int Hq, Hkv, G, tile_tok, causal, box;
+  float scale_log2;
+  float* part;       // partial rows of units cut between CTAs, 2 slots a CTA, 2 tiles a slot
+  uint32_t* pflags;  // [CTAs][2] publication flags, tagged per call
+  uint32_t tag;
+};
+
+// keys that tokens up to tok_end (exclusive) of a sequence of nq new tokens and len keys see, in
+// 128-key blocks, at least one
+__host__ __device__ __forceinline__ int blocks_seen(int len, int nq, int tok_end, int causal) {
+  const int last = causal ? len - nq + min(tok_end, nq) : len;
+  return max(1, (max(0, min(len, last)) + kBN - 1) / kBN);
+}
+
+struct SeqInfo {
+  int start, nq, len;
+};
+
+// first step of CTA c's run: W steps over n CTAs
+__device__ __forceinline__ int64_t run_start(int c, int64_t W, int n) {
+  return c >= n ? W : static_cast<int64_t>(c) * W / n;
+}
+__device__ __forceinline__ int run_of(int64_t t, int64_t W, int n) {
+  return static_cast<int>(((t + 1) * n - 1) / W);
+}
+// partial slot of CTA c's piece of a unit: 0 when its run begins in the unit, 1 otherwise
+__device__ __forceinline__ int run_slot(int c, int64_t unit_start, int64_t W, int n) {
+  return run_start(c, W, n) >= unit_start ? 0 : 1;
+}
+// one tile of a piece, column-major: [D + 2 columns][128 rows] f32, columns O[0..D), frame, row sum
+template <int D>
+__device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t) {
+  return part + ((static_cast<int64_t>(c) * 2 + slot) * 2 + t) * (D + 2) * kBM;
+}
+
+// Epilogue of one piece of a unit cut between CTAs, run by all softmax threads: store this row's
+// (O, frame, row sum), release O, publish the piece's flag, and merge all pieces if this CTA finds
+// them all published.  Of two pieces published at the same time at least one sees the other's flag
+// (release store, then a sequentially consistent fence before the flag loads), so at least one CTA
+// merges; every CTA that does writes the same bytes.  Both CTA-wide waits are bounded mbarriers.
+// Returns false if one gave up.
+template <int D, bool BF16>
+__device__ __noinline__ bool paged_piece(const PArgs& args, int64_t W, int n_ctas,
+                                         const PSeg* sgp, uint32_t ocol, bool active, bool valid,
+                                         float f, float l, uint32_t bar0, int pseg,
+                                         volatile int* abort_flag,
+                                         volatile uint32_t* merge_flag) {
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int t = (warp >= 8) ? 1 : 0;
+  const int row = 32 * (warp & 3) + lane;
+  const int cta = static_cast<int>(blockIdx.x);
+  const int64_t unit_start = sgp->unit_start;
+  const int slot = run_slot(cta, unit_start, W, n_ctas);
+  const int ntok = t ? sgp->tokB : sgp->tokA;
+  const int rows = ntok * args.G;  // rows of this tile in use
+  if (32 * (warp & 3) < rows) {
+    float* pt = piece_tile<D>(args.part, cta, slot, t) + row;
+    const bool have = active && f != -INFINITY;
+    if (active) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(ocol + 32 * c, r);
+        tmem_wait_ld();
+        reg_fence32(r);
+        if (valid) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) pt[(32 * c + i) * kBM] = __uint_as_float(r[i]);
+        }
+      }
+    }
+    if (valid) {
+      pt[D * kBM] = have ? f : -INFINITY;
+      pt[(D + 1) * kBM] = have ? l : 0.f;
+    }
+  }
+  if (active) {
+    tc_fence_before();
+    mbar_arrive(bar0 + 8u * (pbOFree + t));
+  }
+  const int c_first = run_of(unit_start, W, n_ctas);
+  const int c_last = run_of(unit_start + sgp->nb - 1, W, n_ctas);
+  mbar_arrive(bar0 + 8u * pbPiece);
+  if (warp == 4) {
+    bool okw = mbar_wait(bar0 + 8u * pbPiece, pseg & 1, abort_flag, &g_prefill_paged_error);
+    okw = __all_sync(0xffffffffu, okw);
+    bool all = false;
+    if (okw) {
+      if (lane == 0) st_release_gpu(args.pflags + 2 * cta + slot, args.tag);
+      __syncwarp();
+      fence_sc_gpu();
+      all = true;
+      for (int c = c_first + lane; c <= c_last; c += 32)
+        all = all && ld_relaxed_gpu(args.pflags + 2 * c + run_slot(c, unit_start, W, n_ctas)) ==
+                         args.tag;
+      all = __all_sync(0xffffffffu, all);
+      if (all) fence_acq_rel_gpu();
+    }
+    if (lane == 0) {
+      *merge_flag = all ? 1u : 0u;
+      mbar_arrive(bar0 + 8u * pbDecided);
+    }
+  }
+  const bool ok = mbar_wait(bar0 + 8u * pbDecided, pseg & 1, abort_flag, &g_prefill_paged_error);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  if (*merge_flag == 0u) return true;
+  // frame F = max over the pieces, weights 2^(f_p - F), pieces in CTA order.  Rp rows across the
+  // lanes, so that a piece's column is read as one run; the tile's 128 threads share the columns
+  // out when there are fewer rows than threads.
+  const int Rp = rows > 64 ? 128 : rows > 32 ? 64 : 32;
+  const int u = 32 * (warp & 3) + lane;
+  const int r = u % Rp, cg = u / Rp;
+  if (rows > 0 && r < rows) {
+    auto tile_of = [&](int c) -> const float* {
+      return piece_tile<D>(args.part, c, run_slot(c, unit_start, W, n_ctas), t) + r;
+    };
+    float F = -INFINITY;
+#pragma unroll 4
+    for (int c = c_first; c <= c_last; ++c) F = fmaxf(F, __ldcg(tile_of(c) + D * kBM));
+    float L = 0.f;
+#pragma unroll 4
+    for (int c = c_first; c <= c_last; ++c) {
+      const float* pc = tile_of(c);
+      const float fp = __ldcg(pc + D * kBM), lp = __ldcg(pc + (D + 1) * kBM);
+      if (fp != -INFINITY) L = fmaf(ex2(fp - F), lp, L);
+    }
+    const float inv_l = F == -INFINITY ? 0.f : 1.f / L;
+    const int tok = r / args.G;
+    uint8_t* orow = args.o + (sgp->row0 + t * args.tile_tok + tok) * args.o_row_stride +
+                    (sgp->g * args.G + (r - tok * args.G)) * args.o_head_stride;
+    const int cols = D * Rp / kBM;  // columns of this thread
+#pragma unroll 1
+    for (int c0 = cg * cols; c0 < (cg + 1) * cols; c0 += 16) {
+      float acc[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+      for (int c = c_first; c <= c_last; c += 2) {
+        // two pieces' loads in flight together
+        const bool two = c < c_last;
+        const float* p0 = tile_of(c);
+        const float* p1 = tile_of(two ? c + 1 : c);
+        const float f0 = __ldcg(p0 + D * kBM), f1 = __ldcg(p1 + D * kBM);
+        float v0[16], v1[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v0[i] = __ldcg(p0 + (c0 + i) * kBM);
+          v1[i] = __ldcg(p1 + (c0 + i) * kBM);
+        }
+        if (f0 != -INFINITY) {
+          const float w = ex2(f0 - F);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v0[i], acc[i]);
+        }
+        if (two && f1 != -INFINITY) {
+          const float w = ex2(f1 - F);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v1[i], acc[i]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pk[i] = pack2<BF16>(acc[8 * h + 2 * i] * inv_l, acc[8 * h + 2 * i + 1] * inv_l);
+        *reinterpret_cast<uint4*>(orow + (c0 + 8 * h) * 2) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+    }
+  }
+  if (warp == 4) {
+    // clear the unit's flags for the next call (or graph replay) with this tag
+    for (int c = c_first + lane; c <= c_last; c += 32)
+      st_relaxed_gpu(args.pflags + 2 * c + run_slot(c, unit_start, W, n_ctas), 0u);
+  }
+  return true;
+}
+
+template <int D, bool BF16, bool KQ4, bool VQ4>
+__global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
+    prefill_paged_kernel(const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ PArgs args) {
+  using C = Cfg<D, KQ4, VQ4, true>;
+  constexpr int kChunks = D / 64;  // 64-element column chunks of a tile
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * i; };
+  uint8_t* bgen = sgen + C::kOffBar;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bgen + kOffAbort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bgen + kOffTmem);
+  int64_t* plan = reinterpret_cast<int64_t*>(bgen + kOffPlan);
+  PSeg* segq = reinterpret_cast<PSeg*>(bgen + kOffSegQ);
+  auto seg_at = [&](int i) -> PSeg* {
+    return reinterpret_cast<PSeg*>(bgen + kOffSegQ + (i % kSegQ) * 64);
+  };
+  (void)segq;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(blockIdx.x);
+  const PagedBatch& bt = args.batch;
+  const int cap = bt.page_size * bt.pages_per_seq;
+
+  // ---- the batch, as the scheduling warp reads it
+  auto seq_info = [&](int b) -> SeqInfo {
+    SeqInfo s = {0, 0, 0};
+    if (b < bt.B) {
+      s.start = __ldg(bt.starts + b);
+      s.nq = __ldg(bt.starts + b + 1) - s.start;
+      s.len = max(0, min(__ldg(bt.lens + b), cap));
+    }
+    return s;
+  };
+  const int pair_tok = 2 * args.tile_tok;
+  // steps of a sequence's units for one kv head
+  auto seq_steps = [&](const SeqInfo& s) -> int64_t {
+    int64_t n = 0;
+    for (int t = 0; t < s.nq; t += pair_tok)
+      n += blocks_seen(s.len, s.nq, t + pair_tok, args.causal);
+    return n;
+  };
+
+  if (warp == 0) {
+    // steps in all; a batch description that is not a rising run of rows makes no steps
+    int64_t W = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < bt.B; b0 += 32) {
+      const int b = b0 + lane;
+      if (b < bt.B) {
+        const int v = __ldg(bt.starts + b), next = __ldg(bt.starts + b + 1);
+        const int len = __ldg(bt.lens + b);
+        if (bad_start(v, next, bt.rows)) {
+          bad = true;
+        } else {
+          if (cta == 0 && (len < 0 || len > cap))
+            atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
+          W += seq_steps(seq_info(b)) * args.Hkv;
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
+    if (__any_sync(0xffffffffu, bad)) {
+      if (cta == 0 && lane == 0) atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
+      W = 0;
+    }
+    if (lane == 0) {
+      // one CTA per SM, but never more than steps: a unit's merge waits for every CTA between its
+      // first and its last piece
+      const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
+      plan[0] = W;
+      plan[1] = cta < n ? run_start(cta, W, n) : W;
+      plan[2] = cta < n ? run_start(cta + 1, W, n) : W;
+    }
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
+    if (lane == 0) {
+      mbar_init(bar(pbQFull), 1);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(bar(pbSFull + t), 1);
+        mbar_init(bar(pbPReady + t), 128);
+        mbar_init(bar(pbODone + t), 1);
+        mbar_init(bar(pbOFree + t), 128);
+      }
+      mbar_init(bar(pbDrain), 1);
+      mbar_init(bar(pbQEmpty), 1);
+      mbar_init(bar(pbPiece), 256);
+      mbar_init(bar(pbDecided), 1);
+      mbar_init(bar(pbTail), 1);
+      for (int s = 0; s < kSegQ; ++s) {
+        mbar_init(bar(pbSegFull + s), 1);
+        mbar_init(bar(pbSegEmpty + s), 1 + 8);  // the issuer and the eight softmax warps
+      }
+      for (int s = 0; s < C::kStages; ++s) {
+        const bool q4s = (C::kStages % 2 == 0) ? ((s & 1) ? VQ4 : KQ4) : (KQ4 && VQ4);
+        mbar_init(bar(pbRingFull + s), q4s ? C::kDqThreads : 1);
+        mbar_init(bar(pbRingEmpty + s), 1);
+      }
+      for (int s = 0; s < C::kRawStages; ++s) {
+        mbar_init(bar(pbRawFull + s), 1 + 32);  // TMA lane + 32 cp.async arrivals
+        mbar_init(bar(pbRawEmpty + s), C::kDqThreads);
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // query rows that no token fills (G does not divide 128): zeros, so that their scores are
+    const int used = args.G * args.tile_tok;
+    const int row = threadIdx.x - 128 - (warp >= 8 ? 128 : 0);
+    if (row >= used) {
+      uint8_t* q = sgen + C::kOffQ + (warp >= 8 ? C::kQBytes : 0) + row * 128;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(q + c * (kBM * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t W = plan[0], t_begin = plan[1], t_end = plan[2];
+  const int n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
+
+  // registers moved to the softmax warpgroups with a q4_0 side, as in fa_prefill.cu
+  if (warp < 4 || warp >= 12) {
+    if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0) {
+      // -------------------------------------------------- scheduler and producer
+      if (lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+      }
+      bool ok = true;
+      // the unit of step t_begin: sequence, first token of the pair, kv head
+      int b = 0, tok = 0, g = 0;
+      int64_t u0 = 0;  // global step of the unit's block 0
+      SeqInfo sq = {0, 0, 0};
+      int nb = 1;
+      if (t_begin < t_end) {
+        for (int b0 = 0; b0 < bt.B; b0 += 32) {
+          const int64_t own = seq_steps(seq_info(b0 + lane)) * args.Hkv;
+          int64_t end = own;  // inclusive scan over the lanes
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
+            if (lane >= off) end += x;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, u0 + end > t_begin);
+          if (past) {
+            const int who = __ffs(past) - 1;
+            u0 += __shfl_sync(0xffffffffu, end - own, who);
+            b = b0 + who;
+            break;
+          }
+          u0 += __shfl_sync(0xffffffffu, end, 31);
+        }
+        sq = seq_info(b);
+        nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
+        while (t_begin >= u0 + static_cast<int64_t>(nb) * args.Hkv) {
+          u0 += static_cast<int64_t>(nb) * args.Hkv;
+          tok += pair_tok;
+          nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
+        }
+        g = static_cast<int>((t_begin - u0) / nb);
+        u0 += static_cast<int64_t>(g) * nb;
+      }
+
+      int n = 0;      // ring tiles
+      int rt = 0;     // raw q4_0 tiles
+      int pg = 0;     // paired ring: slots filled
+      int qn = 0;     // Q loads issued
+      int tails = 0;  // V tiles cleared past the sequence's end
+      const int nbox = kBN / args.box;
+      // the row of the tensor map's third dimension (page, kv head) that holds keys
+      // [j * 128 + i * box, + box) of the sequence, or -1: nothing there (TMA fills with zeros)
+      auto box_at = [&](int j, int i, int& row) -> int {
+        const int key = j * kBN + i * args.box;
+        row = 0;
+        if (i >= nbox || key >= sq.len) return -1;
+        const int lp = key / bt.page_size;
+        row = key - lp * bt.page_size;
+        const int page = __ldg(bt.table + static_cast<int64_t>(b) * bt.pages_per_seq + lp);
+        if (page < 0 || page >= bt.num_pages) {
+          atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
+          return -1;
+        }
+        return page * args.Hkv + g;
+      };
+      // dense tile boxes: lane (box, chunk) of 16 copies one box's 64 columns
+      auto copy_dense = [&](const CUtensorMap* tm, uint32_t dst, uint32_t full, int at, int row,
+                            int i, int c) {
+        tma_load_3d(dst + c * (kBN * 128) + i * args.box * 128, tm, full, c * 64, row, at);
+      };
+      // rows [len, end of its box) of a dense V tile hold no key: clear them once the tile has
+      // landed (only the last block of a sequence has such rows)
+      auto tail_rows = [&](int j) -> int {  // first such row of the tile, kBN if none
+        const int r0 = sq.len - j * kBN;
+        return (r0 > 0 && r0 < kBN && r0 % args.box != 0) ? r0 : kBN;
+      };
+      auto clear_tail = [&](uint32_t stage, int r0) -> bool {
+        bool w = mbar_wait(bar(pbTail), tails & 1, abort_flag, &g_prefill_paged_error);
+        w = __all_sync(0xffffffffu, w);
+        if (!w) return false;
+        const int r1 = (r0 + args.box - 1) / args.box * args.box;
+        uint8_t* p = sgen + (stage - sbase);
+        for (int i = lane; i < (r1 - r0) * kChunks * 8; i += 32) {
+          const int c = i / ((r1 - r0) * 8), k = i - c * ((r1 - r0) * 8);
+          *reinterpret_cast<uint4*>(p + c * (kBN * 128) + r0 * 128 + k * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        ++tails;
+        return true;
+      };
+      const int di = (lane % 16) / kChunks, dc = (lane % 16) % kChunks;  // dense box and chunk
+      // one slot of the paired ring: K of block kj (if >= 0) by lanes 0-15, V of block vj by 16-31
+      auto produce_pair = [&](int kj, int vj) {
+        const bool vhalf = lane >= 16;
+        const int j = vhalf ? vj : kj;
+        int row = 0, at = -1;
+        if (j >= 0) at = box_at(j, di, row);
+        const int p = pg % C::kSlots;
+        if (lane == 0 && pg >= C::kSlots)
+          ok = mbar_wait(bar(pbRingEmpty + p), ((pg / C::kSlots) - 1) & 1, abort_flag,
+                         &g_prefill_paged_error);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) return;
+        const uint32_t dst = sbase + C::kOffRing + 2 * p * C::kTileBytes;
+        const int r0 = vj >= 0 ? tail_rows(vj) : kBN;
+        if (lane == 0) {
+          const int direct = (kj >= 0 ? 1 : 0) + (vj >= 0 && r0 == kBN ? 1 : 0);
+          if (r0 < kBN) mbar_arrive_expect_tx(bar(pbTail), C::kTileBytes);
+          if (r0 == kBN) mbar_arrive_expect_tx(bar(pbRingFull + p), direct * C::kTileBytes);
+        }
+        __syncwarp();
+        if (j >= 0 && di < nbox)
+          copy_dense(vhalf ? &tm_v : &tm_k, dst + (vhalf ? C::kTileBytes : 0),
+                     r0 < kBN ? bar(pbTail) : bar(pbRingFull + p), at, row, di, dc);
+        if (r0 < kBN) {
+          // (kj < 0 here: the tail is in the sequence's last block)
+          ok = clear_tail(dst + C::kTileBytes, r0);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive(bar(pbRingFull + p));
+        }
+        ++pg;
+      };
+      // one tile of the unpaired ring (a q4_0 side)
+      auto produce = [&](bool is_v, int j) {
+        if (!ok) return;
+        if (!(is_v ? VQ4 : KQ4)) {
+          const int s = n % C::kStages;
+          int row = 0;
+          const int at = lane < 16 ? box_at(j, di, row) : -1;
+          if (lane == 0 && n >= C::kStages)
+            ok = mbar_wait(bar(pbRingEmpty + s), ((n / C::kStages) - 1) & 1, abort_flag,
+                           &g_prefill_paged_error);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) return;
+          const uint32_t dst = sbase + C::kOffRing + s * C::kTileBytes;
+          const int r0 = is_v ? tail_rows(j) : kBN;
+          const uint32_t full = r0 < kBN ? bar(pbTail) : bar(pbRingFull + s);
+          if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+          __syncwarp();
+          if (lane < 16 && di < nbox)
+            copy_dense(is_v ? &tm_v : &tm_k, dst, full, at, row, di, dc);
+          if (r0 < kBN) {
+            ok = clear_tail(dst, r0);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive(bar(pbRingFull + s));
+          }
+        } else if constexpr (C::kAnyQ4) {
+          const int s = rt % C::kRawStages;
+          int row = 0;
+          const int at = box_at(j, lane, row);
+          if (lane == 0 && rt >= C::kRawStages)
+            ok = mbar_wait(bar(pbRawEmpty + s), ((rt / C::kRawStages) - 1) & 1, abort_flag,
+                           &g_prefill_paged_error);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) return;
+          const uint32_t dst = sbase + C::kOffRaw + s * C::kRawBytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar(pbRawFull + s), C::kRawNib);
+          __syncwarp();
+          if (lane < nbox)
+            tma_load_3d(dst + lane * args.box * C::kNibRow, is_v ? &tm_v : &tm_k,
+                        bar(pbRawFull + s), 0, row, at);
+          // scales: one 4- or 8-byte row per key, zero past the sequence's end
+          const uint8_t* sp = is_v ? args.v_scale : args.k_scale;
+#pragma unroll
+          for (int k = 0; k < kBN / 32; ++k) {
+            const int kr = lane + 32 * k;
+            const int i = kr / args.box;
+            const int kat = __shfl_sync(0xffffffffu, at, i);
+            const int krow = __shfl_sync(0xffffffffu, row, i) + (kr - i * args.box);
+            const bool in = kat >= 0 && j * kBN + kr < sq.len;
+            const uint8_t* src =
+                sp + (in ? (static_cast<int64_t>(kat) * bt.page_size + krow) * C::kScaleRow : 0);
+            const uint32_t d = dst + C::kRawNib + kr * C::kScaleRow;
+            if (C::kScaleRow == 8)
+              cp_async_8(d, src, in ? 8u : 0u);
+            else
+              cp_async_4(d, src, in ? 4u : 0u);
+          }
+          cp_async_mbar_arrive_noinc(bar(pbRawFull + s));
+          ++rt;
+        }
+        ++n;
+      };
+
+      int sidx = 0;
+      int64_t t = t_begin;
+      while (t < t_end && ok) {
+        // the unit (b, tok, g), nb steps from u0: its segment of this run
+        const int tokA = min(args.tile_tok, sq.nq - tok);
+        const int tokB = max(0, min(args.tile_tok, sq.nq - tok - args.tile_tok));
+        const int j0 = static_cast<int>(t - u0);
+        const int j1 = static_cast<int>(min(static_cast<int64_t>(nb), t_end - u0));
+        if (lane == 0 && sidx >= kSegQ)
+          ok = mbar_wait(bar(pbSegEmpty + sidx % kSegQ), ((sidx / kSegQ) - 1) & 1, abort_flag,
+                         &g_prefill_paged_error);
+        if (lane == 0 && ok) {
+          PSeg* s = seg_at(sidx);
+          s->row0 = sq.start + tok;
+          s->g = g;
+          s->tokA = tokA;
+          s->tokB = tokB;
+          s->pos0 = sq.len - sq.nq + tok;
+          s->len = sq.len;
+          s->nbA = blocks_seen(sq.len, sq.nq, tok + args.tile_tok, args.causal);
+          s->nbB = tokB > 0 ? nb : 0;
+          s->nb = nb;
+          s->j0 = j0;
+          s->j1 = j1;
+          s->unit_start = u0;
+          mbar_arrive(bar(pbSegFull + sidx % kSegQ));
+          if (sidx > 0)
+            ok = mbar_wait(bar(pbQEmpty), (sidx - 1) & 1, abort_flag, &g_prefill_paged_error);
+          if (ok) {
+            const uint32_t bytes = kChunks * args.tile_tok * args.G * 128;
+            mbar_arrive_expect_tx(bar(pbQFull), (tokB > 0 ? 2 : 1) * bytes);
+            for (int ti = 0; ti < (tokB > 0 ? 2 : 1); ++ti)
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_3d(sbase + C::kOffQ + ti * C::kQBytes + c * (kBM * 128), &tm_q,
+                            bar(pbQFull), c * 64, g * args.G,
+                            sq.start + tok + ti * args.tile_tok);
+            ++qn;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        if constexpr (C::kPaired) {
+          produce_pair(j0, -1);
+          for (int j = j0; j < j1 && ok; ++j) produce_pair(j + 1 < j1 ? j + 1 : -1, j);
+        } else {
+          for (int j = j0; j < j1 && ok; ++j) {
+            produce(false, j);
+            produce(true, j);
+          }
+        }
+        ++sidx;
+        t = u0 + j1;
+        if (t < t_end) {  // the next unit
+          u0 += nb;
+          if (++g == args.Hkv) {
+            g = 0;
+            tok += pair_tok;
+            while (tok >= sq.nq && b + 1 < bt.B) {
+              sq = seq_info(++b);
+              tok = 0;
+            }
+            nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
+          }
+        }
+      }
+      if (ok && t_begin < t_end && lane == 0) {
+        // end of the run
+        if (sidx >= kSegQ)
+          ok = mbar_wait(bar(pbSegEmpty + sidx % kSegQ), ((sidx / kSegQ) - 1) & 1, abort_flag,
+                         &g_prefill_paged_error);
+        if (ok) {
+          seg_at(sidx)->j1 = -1;
+          mbar_arrive(bar(pbSegFull + sidx % kSegQ));
+        }
+      }
+      if (!ok && lane == 0) {
+        // let copies already issued land before the CTA's shared memory goes away
+        volatile int never = 0;
+        if (qn > 0) mbar_wait(bar(pbQFull), (qn - 1) & 1, &never, nullptr, kWaitLimitNs);
+        if constexpr (C::kPaired) {
+          for (int i = max(0, pg - C::kSlots); i < pg; ++i)
+            mbar_wait(bar(pbRingFull + i % C::kSlots), (i / C::kSlots) & 1, &never, nullptr,
+                      kWaitLimitNs);
+        }
+        for (int i = max(0, n - C::kStages); i < n; ++i)
+          if (!((i & 1) ? VQ4 : KQ4))
+            mbar_wait(bar(pbRingFull + i % C::kStages), (i / C::kStages) & 1, &never, nullptr,
+                      kWaitLimitNs);
+        if constexpr (C::kAnyQ4) {
+          for (int i = max(0, rt - C::kRawStages); i < rt; ++i)
+            mbar_wait(bar(pbRawFull + i % C::kRawStages), (i / C::kRawStages) & 1, &never,
+                      nullptr, kWaitLimitNs);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0 && t_begin < t_end) {
+        constexpr uint32_t idesc_qk = make_idesc_f16(kBM, kBN, BF16, false);
+        constexpr uint32_t idesc_pv = make_idesc_f16(kBM, D, BF16, true);
+        bool ok = true;
+        int n = 0, gn = 0;       // ring tiles / paired slots taken
+        int prA = 0, prB = 0;    // P-ready waits per tile before this segment (barrier phases)
+        int actA = 0, actB = 0;  // earlier segments in which the tile had blocks
+        auto acquire_g = [&]() -> int {
+          const int p = gn % C::kSlots;
+          if (ok) ok = mbar_wait(bar(pbRingFull + p), (gn / C::kSlots) & 1, abort_flag,
+                                 &g_prefill_paged_error);
+          tc_fence_after();
+          ++gn;
+          return p;
+        };
+        auto acquire = [&]() -> int {
+          const int s = n % C::kStages;
+          if (ok) ok = mbar_wait(bar(pbRingFull + s), (n / C::kStages) & 1, abort_flag,
+                                 &g_prefill_paged_error);
+          tc_fence_after();
+          ++n;
+          return s;
+        };
+        auto release = [&](int s) { mma_commit(bar(pbRingEmpty + s)); };
+        auto issue_qk = [&](int t, int s) {
+          const uint32_t qaddr = sbase + C::kOffQ + t * C::kQBytes;
+          const uint32_t kaddr = sbase + C::kOffRing + s * C::kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kBM * 128) + (kk & 3) * 32;
+            mma_ss(tmem + col_s(t), make_sdesc_sw128(qaddr + off, 16, 1024),
+                   make_sdesc_sw128(kaddr + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(pbSFull + t));
+        };
+        auto issue_pv = [&](int t, int j, int s, int j0, int e_t, int pb) {
+          ok = ok && mbar_wait(bar(pbPReady + t), (pb + j) & 1, abort_flag,
+                               &g_prefill_paged_error);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t vaddr = sbase + C::kOffRing + s * C::kTileBytes;
+          const uint32_t ocol = t ? C::kColO1 : C::kColO0;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_ts(tmem + ocol, tmem + col_s(t) + kk * 8,
+                   make_sdesc_sw128(vaddr + kk * (16 * 128), kBN * 128, 1024), idesc_pv,
+                   (j > j0 || kk > 0) ? 1u : 0u);
+          if (j == e_t - 1) mma_commit(bar(pbODone + t));
+        };
+        // per segment: QK_A(j0) QK_B(j0) | PV_A(j) QK_A(j+1) PV_B(j) QK_B(j+1) | ...
+        for (int sidx = 0; ok; ++sidx) {
+          ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
+                         &g_prefill_paged_error);
+          if (!ok) break;
+          const PSeg* sp = seg_at(sidx);
+          const int j0 = sp->j0, j1 = sp->j1;
+          if (j1 < 0) break;
+          const int eA = min(j1, sp->nbA), eB = min(j1, sp->nbB);
+          mbar_arrive(bar(pbSegEmpty + sidx % kSegQ));
+          ok = mbar_wait(bar(pbQFull), sidx & 1, abort_flag, &g_prefill_paged_error);
+          tc_fence_after();
+          if (!ok) break;
+          const int pbA = prA - j0, pbB = prB - j0;
+          if constexpr (C::kPaired) {
+            {
+              const int p = acquire_g();
+              if (!ok) break;
+              if (j0 < eA) issue_qk(0, 2 * p);
+              if (j0 < eB)
+                issue_qk(1, 2 * p);  // tile B's softmax releases the slot
+              else
+                release(p);
+              if (j0 + 1 == j1) mma_commit(bar(pbQEmpty));
+            }
+            if (j0 < eA && actA > 0)
+              ok = ok && mbar_wait(bar(pbOFree + 0), (actA - 1) & 1, abort_flag,
+                                   &g_prefill_paged_error);
+            if (j0 < eB && actB > 0)
+              ok = ok && mbar_wait(bar(pbOFree + 1), (actB - 1) & 1, abort_flag,
+                                   &g_prefill_paged_error);
+            for (int j = j0; j < j1 && ok; ++j) {
+              const int p = acquire_g();
+              const bool next = j + 1 < j1;
+              if (!ok) break;
+              if (j < eA) issue_pv(0, j, 2 * p + 1, j0, eA, pbA);
+              if (!ok) break;
+              if (next && j + 1 < eA) issue_qk(0, 2 * p);
+              if (j < eB) issue_pv(1, j, 2 * p + 1, j0, eB, pbB);
+              if (!ok) break;
+              if (next && j + 1 < eB)
+                issue_qk(1, 2 * p);
+              else
+                release(p);
+              if (next && j + 2 == j1) mma_commit(bar(pbQEmpty));
+            }
+          } else {
+            {
+              const int sK = acquire();
+              if (!ok) break;
+              if (j0 < eA) issue_qk(0, sK);
+              if (j0 < eB) issue_qk(1, sK);
+              release(sK);
+              if (j0 + 1 == j1) mma_commit(bar(pbQEmpty));
+            }
+            if (j0 < eA && actA > 0)
+              ok = ok && mbar_wait(bar(pbOFree + 0), (actA - 1) & 1, abort_flag,
+                                   &g_prefill_paged_error);
+            if (j0 < eB && actB > 0)
+              ok = ok && mbar_wait(bar(pbOFree + 1), (actB - 1) & 1, abort_flag,
+                                   &g_prefill_paged_error);
+            for (int j = j0; j < j1 && ok; ++j) {
+              const int sV = acquire();
+              const bool next = j + 1 < j1;
+              const int sK = next ? acquire() : 0;
+              if (!ok) break;
+              if (j < eA) issue_pv(0, j, sV, j0, eA, pbA);
+              if (!ok) break;
+              if (next && j + 1 < eA) issue_qk(0, sK);
+              if (j < eB) issue_pv(1, j, sV, j0, eB, pbB);
+              if (!ok) break;
+              release(sV);
+              if (next) {
+                if (j + 1 < eB) issue_qk(1, sK);
+                release(sK);
+                if (j + 2 == j1) mma_commit(bar(pbQEmpty));
+              }
+            }
+          }
+          if (j0 < eA) {
+            ++actA;
+            prA += eA - j0;
+          }
+          if (j0 < eB) {
+            ++actB;
+            prB += eB - j0;
+          }
+        }
+        if (!ok) {
+          // wait until every MMA issued so far has finished before TMEM is released
+          volatile int never = 0;
+          mma_commit(bar(pbDrain));
+          mbar_wait(bar(pbDrain), 0, &never, nullptr, kWaitLimitNs);
+        }
+      }
+    } else if constexpr (C::kAnyQ4) {
+      if (C::is_dq_warp(warp)) {
+        // -------------------------------------------------------------- q4_0 dequant
+        const int u = C::dq_index(warp, lane);
+        const uint32_t mg = opaque_u32(BF16 ? 0x43004300u : 0x64006400u);
+        bool ok = true;
+        const int64_t ntiles = 2 * (t_end - t_begin);  // K and V of every step
+        int r = 0;  // raw q4_0 tiles consumed
+        for (int n = 0; n < ntiles; ++n) {
+          if (!((n & 1) ? VQ4 : KQ4)) continue;  // a dense tile: the producer's TMA fills it
+          const int rs = r % C::kRawStages;
+          const int s = n % C::kStages;
+          ok = mbar_wait(bar(pbRawFull + rs), (r / C::kRawStages) & 1, abort_flag,
+                         &g_prefill_paged_error);
+          if (ok && n >= C::kStages)
+            ok = mbar_wait(bar(pbRingEmpty + s), ((n / C::kStages) - 1) & 1, abort_flag,
+                           &g_prefill_paged_error);
+          if (!ok) break;
+          const uint8_t* raw = sgen + C::kOffRaw + rs * C::kRawBytes;
+          uint8_t* dst = sgen + C::kOffRing + s * C::kTileBytes;
+          constexpr int kItems = kBN * (D / 32);
+#pragma unroll
+          for (int k = 0; k < (kItems + C::kDqThreads - 1) / C::kDqThreads; ++k) {
+            const int it = u + k * C::kDqThreads;
+            if (kItems % C::kDqThreads == 0 || it < kItems)
+              dequant_item<D, BF16, C::kNibRow, C::kScaleRow, C::kRawNib>(raw, dst, it % kBN,
+                                                                          it / kBN, mg);
+          }
+          // generic-proxy writes must be visible to the tensor core's async proxy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(bar(pbRingFull + s));
+          mbar_arrive(bar(pbRawEmpty + rs));
+          ++r;
+        }
+      }
+    }
+  } else {
+    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
+    // ---------------------------------------------------------------- softmax rows
+    const int t = (warp >= 8) ? 1 : 0;  // query tile
+    const int row = 32 * (warp & 3) + lane;
+    const int rtok = row / args.G;      // this row's token within the tile
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t scol = tmem + lane_off + col_s(t);
+    const uint32_t ocol = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
+    const float sl2 = args.scale_log2;
+    volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(bgen + kOffMerge);
+    bool ok = true;
+    int sf = 0;    // S-full waits so far (barrier phase)
+    int od = 0;    // segments in which this tile had blocks (O-done phase)
+    int pseg = 0;  // pieces published so far
+    int gn = 0;    // paired ring: slots of the segments before this one
+    for (int sidx = 0; t_begin < t_end; ++sidx) {
+      ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
+                     &g_prefill_paged_error);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const PSeg* sp = seg_at(sidx);
+      const int j1 = sp->j1;
+      if (j1 < 0) break;
+      const int j0 = sp->j0;
+      const int g0 = gn - j0;  // ring slot of the one holding K(j): g0 + j
+      gn += j1 - j0 + 1;
+      const int ntok = t ? sp->tokB : sp->tokA;
+      const int e_t = ntok > 0 ? min(j1, t ? sp->nbB : sp->nbA) : 0;
+      const int len = sp->len;
+      const int first_pos = sp->pos0 + t * args.tile_tok;  // of the tile's first token
+      // last key that this row sees, and the last one that every row of the tile sees
+      const int lim = args.causal ? min(len - 1, first_pos + rtok) : len - 1;
+      const int lim_all = args.causal ? min(len - 1, first_pos) : len - 1;
+      const bool live = 32 * (warp & 3) < ntok * args.G;  // some row of the warp is in use
+      float f = -INFINITY;  // frame, base-2 units of the scaled score
+      float l = 0.f;
+      int nres = 0;
+      float pmx = 0.f;
+      for (int j = j0; j < e_t; ++j) {
+        ok = mbar_wait(bar(pbSFull + t), sf & 1, abort_flag, &g_prefill_paged_error);
+        ++sf;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if constexpr (C::kPaired) {
+          // QK_B of block j done: release the ring slot holding K(j)
+          if (t == 1 && warp == 8 && lane == 0)
+            mbar_arrive(bar(pbRingEmpty + (g0 + j) % C::kSlots));
+        }
+        if (live) {
+          const int kb = j * kBN;
+          softmax_block<D, BF16>(scol, ocol, kb + kBN - 1 > lim_all, lim - kb, sl2, j > j0, f, l,
+                                 nres, pmx);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(pbPReady + t));
+      }
+      if (!ok) break;
+      const bool active = e_t > j0;  // the tile had key blocks in this segment
+      if (active) {
+        ok = mbar_wait(bar(pbODone + t), od & 1, abort_flag, &g_prefill_paged_error);
+        ++od;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const bool valid = rtok < ntok && row < args.G * args.tile_tok;
+      const int64_t unit_start = sp->unit_start;
+      const bool split = run_of(unit_start, W, n_ctas) != run_of(unit_start + sp->nb - 1, W, n_ctas);
+      if (!split) {
+        if (active) {
+          if (live) {
+            const bool none = f == -INFINITY;  // the row sees no key
+            const float inv_l = 1.f / l;
+            uint8_t* orow =
+                args.o + (sp->row0 + t * args.tile_tok + rtok) * args.o_row_stride +
+                (sp->g * args.G + (row - rtok * args.G)) * args.o_head_stride;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(ocol + 32 * c, r);
+              tmem_wait_ld();
+              reg_fence32(r);
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                pk[i] = none ? 0u
+                             : pack2<BF16>(__uint_as_float(r[2 * i]) * inv_l,
+                                           __uint_as_float(r[2 * i + 1]) * inv_l);
+              if (valid) {
+                uint4* dst = reinterpret_cast<uint4*>(orow + c * 64);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              }
+            }
+          }
+          // O has been read out of tensor memory: the next segment's PV may overwrite it
+          tc_fence_before();
+          mbar_arrive(bar(pbOFree + t));
+        }
+      } else {
+        ok = paged_piece<D, BF16>(args, W, n_ctas, sp, ocol, active, valid, f, l, bar0, pseg,
+                                  abort_flag, merge_flag);
+        ++pseg;
+        if (!ok) break;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(pbSegEmpty + sidx % kSegQ));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool BF16, bool KQ4, bool VQ4>
+cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
+  using C = Cfg<D, KQ4, VQ4, true>;
+  static_assert(C::kSmemBytes <= 227 * 1024, "shared memory budget");
+  auto kern = prefill_paged_kernel<D, BF16, KQ4, VQ4>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  PArgs a;
+  a.batch = L.batch;
+  a.o = static_cast<uint8_t*>(L.o);
+  a.o_row_stride = 2 * L.o_row_stride;
+  a.o_head_stride = 2 * L.o_head_stride;
+  a.k_scale = static_cast<const uint8_t*>(L.k_scale);
+  a.v_scale = static_cast<const uint8_t*>(L.v_scale);
+  a.Hq = L.Hq;
+  a.Hkv = L.Hkv;
+  a.G = L.Hq / L.Hkv;
+  a.tile_tok = kBM / a.G;
+  a.causal = L.causal;
+  a.box = paged_prefill_box(L.batch.page_size);
+  a.scale_log2 = L.scale * kLog2e;
+  a.pflags = static_cast<uint32_t*>(L.workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) +
+                                    (static_cast<size_t>(L.num_sms) * 2 * sizeof(uint32_t) + 255) /
+                                        256 * 256);
+  a.tag = L.tag;
+  kern<<<L.num_sms, C::kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, a);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_fmt(const PagedPrefillLaunch& L, cudaStream_t stream) {
+  if (L.kq4) return L.vq4 ? launch_t<D, BF16, true, true>(L, stream)
+                          : launch_t<D, BF16, true, false>(L, stream);
+  return L.vq4 ? launch_t<D, BF16, false, true>(L, stream)
+               : launch_t<D, BF16, false, false>(L, stream);
+}
+
+}  // namespace
+
+int paged_prefill_box(int page_size) {
+  int box = 16;
+  while (box < kBN && page_size % (2 * box) == 0) box *= 2;
+  return box;
+}
+
+// publication flags, then the partial rows: two slots of two tiles for every CTA
+size_t paged_prefill_workspace(int D, int num_sms) {
+  const size_t n = static_cast<size_t>(num_sms);
+  return (n * 2 * sizeof(uint32_t) + 255) / 256 * 256 + n * 4 * (D + 2) * kBM * sizeof(float);
+}
+
+cudaError_t paged_prefill_launch(const PagedPrefillLaunch& L, cudaStream_t stream) {
+  if (L.D == 128)
+    return L.bf16 ? launch_fmt<128, true>(L, stream) : launch_fmt<128, false>(L, stream);
+  return L.bf16 ? launch_fmt<64, true>(L, stream) : launch_fmt<64, false>(L, stream);
+}
+
+uint32_t paged_prefill_take_error() {
+  uint32_t v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prefill_paged_error, sizeof(v)) != cudaSuccess)
+    return 0xffffffffu;
+  const uint32_t z = 0;
+  cudaMemcpyToSymbol(g_prefill_paged_error, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fa

@@ -1,0 +1,288 @@
+"""Ragged prefill over page pools (fa_prefill_paged) against the f64 oracle, every element.  Slots
+that hold no token are NaN throughout, so a result that touched one would show it.  Tolerance:
+gpu_common.check_close -- the kernel rounds P once before the PV contraction, a q4_0 side once when
+dequantized and O once when stored, as the prefill kernels it is stated for."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_common import check_close, np64
+from paged_common import DT, make_ragged
+
+pytestmark = pytest.mark.gpu
+
+
+def make_q(rows, Hq, D, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(rows, Hq, D, generator=g).to(DT[dtype])
+
+
+def expected(r, q, causal=True, scale=None):
+    """{sequence: [n, Hq, D] f64}; rows that see no key are zeros."""
+    out = {}
+    D = q.shape[-1]
+    for b, (n, length) in enumerate(zip(r.new, r.lens)):
+        if n == 0:
+            continue
+        s = int(r.starts[b])
+        want = np.zeros((n, q.shape[1], D))
+        blind = min(n, max(0, n - length) if causal else (n if length == 0 else 0))
+        if blind < n:
+            qs = np64(q[s + blind:s + n]).transpose(1, 0, 2)[None]
+            o = oracle.attention(np.ascontiguousarray(qs), r.sequence("k", b)[None],
+                                 r.sequence("v", b)[None], causal=causal,
+                                 q_pos_offset=max(0, length - n) if causal else 0,
+                                 scale=scale or D ** -0.5)
+            want[blind:] = o[0].transpose(1, 0, 2)
+        out[b] = want
+    return out
+
+
+def check(r, q, o, causal=True, scale=None):
+    q4 = "q4_0" in (r.kf, r.vf)
+    for b, want in expected(r, q, causal, scale).items():
+        s = int(r.starts[b])
+        got = np64(o[s:s + r.new[b]])
+        blind = np.all(want == 0, axis=-1)
+        assert (got[blind] == 0).all(), f"sequence {b}: a row without keys is not zero"
+        check_close(got[~blind], want[~blind], r.dtype, f"sequence {b} ({r.new[b]} of {r.lens[b]})",
+                    q4=q4)
+
+
+def run(fa, r, q, **kw):
+    o = fa.fa_prefill_paged(q.cuda(), r.pool(fa, "k"), r.pool(fa, "v"), *r.batch(), **kw)
+    assert fa.fa_get_status() == fa.FA_OK
+    return o
+
+
+CASES = [
+    # new, lens, Hq, Hkv, D, page, dtype, kf, vf
+    ([1], [1], 8, 2, 128, 128, "f16", "dense", "dense"),
+    ([1], [1], 8, 2, 128, 128, "f16", "q4_0", "q4_0"),
+    ([5], [133], 8, 2, 128, 64, "f16", "dense", "dense"),
+    ([40], [300], 8, 2, 128, 128, "bf16", "q4_0", "q4_0"),
+    ([200], [200], 8, 8, 64, 16, "bf16", "dense", "dense"),
+    ([1, 0, 300, 1, 17], [777, 50, 300, 1, 1029], 32, 8, 128, 16, "f16", "dense", "dense"),
+    ([1, 0, 300, 1, 17], [777, 50, 300, 1, 1029], 32, 8, 128, 128, "f16", "q4_0", "q4_0"),
+    ([64, 65, 63, 1, 128, 129], [64, 1000, 63, 4096, 256, 1300], 16, 2, 64, 128, "f16", "q4_0",
+     "dense"),
+    ([33, 1, 500], [1111, 2, 700], 12, 4, 128, 48, "bf16", "dense", "q4_0"),
+    ([7, 90], [5000, 91], 20, 4, 128, 32, "f16", "q4_0", "dense"),
+    ([257, 3], [600, 3], 7, 1, 64, 256, "bf16", "q4_0", "q4_0"),
+    ([31, 2], [2049, 129], 48, 1, 128, 64, "f16", "dense", "dense"),
+    ([3, 2], [513, 40], 128, 1, 64, 16, "f16", "dense", "q4_0"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[2:])) + f"-{c[0]}")
+def test_matches_oracle(fa, case):
+    new, lens, Hq, Hkv, D, page, dtype, kf, vf = case
+    r = make_ragged(new, lens, Hkv, D, page, dtype, kf, vf, seed=sum(lens) + page)
+    q = make_q(sum(new), Hq, D, dtype, seed=3)
+    check(r, q, run(fa, r, q))
+
+
+@pytest.mark.parametrize("kf,vf", [("dense", "dense"), ("q4_0", "q4_0")])
+def test_many_short_sequences(fa, kf, vf):
+    """More units than CTAs times any queue: 150 sequences of a few keys, so that a CTA's run holds
+    many segments."""
+    rng = np.random.default_rng(7)
+    new = [int(x) for x in rng.integers(0, 4, 150)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 200, 150))]
+    r = make_ragged(new, lens, 8, 128, 128, "f16", kf, vf, seed=11)
+    q = make_q(sum(new), 32, 128, "f16", seed=12)
+    check(r, q, run(fa, r, q))
+
+
+@pytest.mark.parametrize("kf,vf", [("dense", "dense"), ("q4_0", "dense"), ("q4_0", "q4_0")])
+def test_one_long_sequence_split_over_all_ctas(fa, kf, vf):
+    """One token over 40 000 keys and one kv head: the unit is cut into a piece per CTA."""
+    r = make_ragged([1], [40003], 1, 128, 128, "bf16", kf, vf, seed=21)
+    q = make_q(1, 4, 128, "bf16", seed=22)
+    check(r, q, run(fa, r, q))
+
+
+@pytest.mark.parametrize("kf", ["dense", "q4_0"])
+def test_rows_without_keys_are_zero(fa, kf):
+    """More rows than tokens (positions below 0) and sequences without any key."""
+    r = make_ragged([5, 3, 200, 2], [2, 0, 60, 900], 2, 64, 128, "f16", kf, kf, seed=31)
+    q = make_q(210, 8, 64, "f16", seed=32)
+    check(r, q, run(fa, r, q))
+    r0 = make_ragged([4, 1], [0, 0], 2, 64, 128, "f16", kf, kf, seed=33)
+    o = run(fa, r0, make_q(5, 8, 64, "f16", seed=34), o=torch.ones(5, 8, 64).half().cuda())
+    assert (o == 0).all()
+
+
+@pytest.mark.parametrize("kf,vf", [("dense", "dense"), ("q4_0", "q4_0")])
+def test_without_the_causal_mask(fa, kf, vf):
+    r = make_ragged([70, 1, 3, 2], [300, 129, 1, 0], 2, 128, 64 if kf == "dense" else 128, "f16",
+                    kf, vf, seed=41)
+    q = make_q(76, 8, 128, "f16", seed=42)
+    check(r, q, run(fa, r, q, causal=False, scale=0.03), causal=False, scale=0.03)
+
+
+def test_score_ramp_moves_frames(fa):
+    """Scores that grow by 2 a key block push the rows' frames past the 10-point margin every few
+    blocks, also across the pieces of units cut between CTAs."""
+    n, length, D = 300, 6000, 128
+    r = make_ragged([n], [length], 2, D, 128, "f16", "dense", "dense", seed=51, poison=False)
+    for p in range(r.table.shape[1]):
+        r.k[int(r.table[0, p]), :, :, 0] = 2.0 * p / (8.0 * D ** -0.5)
+    q = make_q(n, 8, D, "f16", seed=52)
+    q[..., 0] = 8.0
+    check(r, q, run(fa, r, q))
+
+
+def test_strides_and_padding(fa):
+    """q cut out of a fused projection, o head-major, rows before the first sequence and behind the
+    last one: those rows stay as they were."""
+    new, lens, Hq, Hkv, D = [9, 1, 30], [200, 77, 30], 8, 2, 128
+    first, pad = 3, 6
+    rows = first + sum(new) + pad
+    r = make_ragged(new, lens, Hkv, D, 64, "f16", "dense", "dense", seed=61, first_row=first)
+    fused = make_q(rows, Hq + 2 * Hkv, D, "f16", seed=62).cuda()
+    q = fused[:, :Hq]
+    o = torch.full((Hq, rows, D), 7.0, dtype=torch.float16, device="cuda").transpose(0, 1)
+    out = fa.fa_prefill_paged(q, r.pool(fa, "k"), r.pool(fa, "v"), *r.batch(), o)
+    assert fa.fa_get_status() == fa.FA_OK and out is o
+    check(r, q.cpu(), o.cpu())
+    assert (o[:first] == 7.0).all() and (o[first + sum(new):] == 7.0).all()
+    dense = fa.fa_prefill_paged(q.contiguous(), r.pool(fa, "k"), r.pool(fa, "v"), *r.batch())
+    assert torch.equal(dense[first:first + sum(new)], o[first:first + sum(new)])
+    assert (dense[:first] == 0).all() and (dense[first + sum(new):] == 0).all()
+
+
+def test_agrees_with_the_contiguous_prefill_and_the_paged_decode(fa):
+    """One chunk over pages in order is fa_fwd's chunk over the same cache; one token per sequence is
+    fa_decode_paged's call.  Both kernels are compared with the same oracle elsewhere; here within
+    twice its bound, u = 2^-11 on each side."""
+    D, page = 128, 128
+    r = make_ragged([260], [1500], 2, D, page, "f16", "dense", "dense", seed=71, poison=False)
+    q = make_q(260, 8, D, "f16", seed=72).cuda()
+    o = run(fa, r, q)
+    k, v = (torch.from_numpy(r.sequence(s, 0)).half().cuda()[None].contiguous() for s in "kv")
+    ref = fa.fa_fwd(q.transpose(0, 1)[None].contiguous(), k, v)[0].transpose(0, 1)
+    want = expected(r, q.cpu())[0]
+    rms = np.sqrt(np.mean(want ** 2, -1, keepdims=True))
+    assert (np.abs(np64(o) - np64(ref)) <= 2 * 2.0 ** -11 * (np.abs(want) + 6 * rms)).all()
+    r = make_ragged([1] * 5, [300, 1, 129, 2000, 128], 2, D, page, "f16", "q4_0", "q4_0", seed=73)
+    q = make_q(5, 8, D, "f16", seed=74).cuda()
+    o = run(fa, r, q)
+    table, _, lens = r.batch()
+    ref = fa.fa_decode_paged(q[:, :, None].contiguous(), r.pool(fa, "k"), r.pool(fa, "v"), table,
+                             lens)[:, :, 0]
+    for b, want in expected(r, q.cpu()).items():
+        rms = np.sqrt(np.mean(want ** 2, -1, keepdims=True))
+        assert (np.abs(np64(o[b:b + 1]) - np64(ref[b:b + 1]))
+                <= 2 * 2.0 ** -11 * (np.abs(want) + 9 * rms)).all()
+
+
+def test_repeated_calls_are_bitwise_equal_with_a_stale_workspace(fa):
+    r = make_ragged([1, 300, 1, 40], [5000, 4000, 3, 900], 8, 128, 128, "f16", "dense", "dense",
+                    seed=81)
+    q = make_q(342, 32, 128, "f16", seed=82).cuda()
+    k, v, batch = r.pool(fa, "k"), r.pool(fa, "v"), r.batch()
+    ws = torch.full((fa.fa_prefill_paged_workspace_bytes(32, 8, 128),), 255, dtype=torch.uint8,
+                    device="cuda")
+    first = fa.fa_prefill_paged(q, k, v, *batch, workspace=ws)
+    check(r, q.cpu(), first.cpu())
+    for _ in range(8):
+        assert torch.equal(first, fa.fa_prefill_paged(q, k, v, *batch, workspace=ws))
+    assert fa.fa_get_status() == fa.FA_OK
+
+
+def test_captured_call_serves_other_batches(fa):
+    """A captured call replayed after row_starts, seq_lens, the table and q were rewritten, and a
+    second graph over the same workspace in between."""
+    D = 128
+    batches = [([1, 200, 0, 7], [900, 200, 5, 2000]), ([3, 3, 201, 1], [3, 4000, 300, 1]),
+               ([0, 0, 1, 0], [0, 0, 640, 0])]
+    rs = [make_ragged(n, l_, 8, D, 128, "bf16", "q4_0", "dense", seed=90 + i, spare=60 - sum(
+        -(-x // 128) for x in l_)) for i, (n, l_) in enumerate(batches)]
+    pps = max(r.table.shape[1] for r in rs)
+    rows = 208
+    q = torch.zeros(rows, 32, D, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros_like(q)
+    o2 = torch.zeros_like(q)
+    k, v = rs[0].pool(fa, "k"), rs[0].pool(fa, "v")
+    table = torch.zeros(4, pps, dtype=torch.int32, device="cuda")
+    starts = torch.zeros(5, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fa.fa_prefill_paged_workspace_bytes(32, 8, D), dtype=torch.uint8,
+                     device="cuda")
+    side = torch.cuda.Stream()
+    graphs = []
+    for out in (o, o2):
+        g = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=side):
+            fa.fa_prefill_paged(q, k, v, table, starts, lens, out, workspace=ws)
+        graphs.append(g)
+    for i, r in enumerate(rs + rs[:1]):
+        x = make_q(rows, 32, D, "bf16", seed=95 + i)
+        q.copy_(x)
+        k.buf.copy_(r.k)
+        v.copy_(r.v)
+        table.zero_()
+        table[:, :r.table.shape[1]] = r.table.cuda()
+        starts.copy_(r.starts)
+        lens.copy_(torch.tensor(r.lens, dtype=torch.int32))
+        o.fill_(5.0)
+        o2.fill_(5.0)
+        for g in graphs:
+            g.replay()
+        assert fa.fa_get_status() == fa.FA_OK
+        check(r, x, o.cpu())
+        assert torch.equal(o, o2) and (o[sum(r.new):] == 5.0).all()
+
+
+def test_other_stream_allocates_there(fa):
+    r = make_ragged([300], [4000], 8, 128, 128, "f16", "dense", "dense", seed=101)
+    q, k, v, batch = (make_q(300, 32, 128, "f16", seed=102).cuda(), r.pool(fa, "k"),
+                      r.pool(fa, "v"), r.batch())
+    want = fa.fa_prefill_paged(q, k, v, *batch)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        outs.append(fa.fa_prefill_paged(q, k, v, *batch, stream=side))
+        torch.empty(50 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # the other stream's
+    outs.append(fa.fa_prefill_paged(q, k, v, *batch, stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in outs)
+
+
+def test_bad_batches_are_reported(fa):
+    """Row starts out of order or past the tensors: nothing is written.  A page outside the pool and a
+    length past the table: recorded, the rest of the batch is right."""
+    r = make_ragged([4, 9], [300, 200], 2, 128, 128, "f16", "dense", "dense", seed=111)
+    q = make_q(13, 8, 128, "f16", seed=112).cuda()
+    k, v, (table, starts, lens) = r.pool(fa, "k"), r.pool(fa, "v"), r.batch()
+    for bad in ([0, 9, 4], [-1, 4, 13], [0, 4, 14], [5, 4, 13]):
+        o = torch.full_like(q, 3.0)
+        fa.fa_prefill_paged(q, k, v, table, torch.tensor(bad, dtype=torch.int32, device="cuda"),
+                            lens, o)
+        assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
+        assert (o == 3.0).all()
+    for page in (r.shape[0], -1, 1 << 30):
+        t = table.clone()
+        t[0, 1] = page
+        o = fa.fa_prefill_paged(q, k, v, t, starts, lens)
+        assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
+        check_close(np64(o[4:]), expected(r, q.cpu())[1], "f16", "the other sequence")
+    for n in (-1, 128 * table.shape[1] + 1):
+        o = fa.fa_prefill_paged(q, k, v, table, starts,
+                                torch.tensor([n, 200], dtype=torch.int32, device="cuda"))
+        assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
+        check_close(np64(o[4:]), expected(r, q.cpu())[1], "f16", "the other sequence")
+    o = fa.fa_prefill_paged(q, k, v, table, starts, lens)
+    assert fa.fa_get_status() == fa.FA_OK
+
+
+def test_no_rows(fa):
+    r = make_ragged([0, 0], [5, 0], 2, 128, 128, "f16", "dense", "dense", seed=121)
+    o = run(fa, r, make_q(0, 8, 128, "f16", seed=122))
+    assert o.shape == (0, 8, 128)
+    o = run(fa, r, make_q(3, 8, 128, "f16", seed=123))  # padding only
+    assert (o == 0).all()
