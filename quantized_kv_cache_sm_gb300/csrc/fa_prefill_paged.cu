@@ -65,7 +65,7 @@ constexpr int kSegQ = 4;
 constexpr int kOffTmem = pbCount * 8;
 constexpr int kOffAbort = kOffTmem + 8;
 constexpr int kOffMerge = kOffAbort + 8;
-constexpr int kOffPlan = kOffMerge + 8;  // int64: steps in all, this CTA's first and end step
+constexpr int kOffPlan = kOffMerge + 8;  // int64: steps of this CTA's run
 constexpr int kOffSegQ = 512;            // the segment queue
 
 // one segment: steps [j0, j1) of a unit
@@ -75,9 +75,10 @@ struct PSeg {
   int tokA, tokB; // tokens of the tiles (0: tile absent)
   int pos0;       // position of tile A's first token
   int len;        // keys of the sequence
-  int nbA, nbB, nb;  // key blocks of the tiles and of the unit
+  int nbA, nbB;   // key blocks of the tiles
   int j0, j1;     // j1 = -1: no more segments
-  int64_t unit_start;  // global step of the unit's block 0
+  int c_first, c_last;  // CTAs of the unit's first and last step (equal: not cut)
+  int slot_first;       // partial slot of the first one's piece (the others' is 0)
 };
 static_assert(sizeof(PSeg) <= 64 && kOffSegQ + kSegQ * 64 <= 512 + 1024, "segment queue");
 
@@ -105,21 +106,107 @@ struct SeqInfo {
   int start, nq, len;
 };
 
-// first step of CTA c's run: W steps over n CTAs
-__device__ __forceinline__ int64_t run_start(int c, int64_t W, int n) {
-  return c >= n ? W : static_cast<int64_t>(c) * W / n;
+// Division of step counts, which rarely pass 32 bits: a 64-bit division costs some hundred
+// instructions of the scheduling lane.
+__device__ __forceinline__ int64_t div_steps(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
-__device__ __forceinline__ int run_of(int64_t t, int64_t W, int n) {
-  return static_cast<int>(((t + 1) * n - 1) / W);
-}
-// partial slot of CTA c's piece of a unit: 0 when its run begins in the unit, 1 otherwise
-__device__ __forceinline__ int run_slot(int c, int64_t unit_start, int64_t W, int n) {
-  return run_start(c, W, n) >= unit_start ? 0 : 1;
-}
-// one tile of a piece, column-major: [D + 2 columns][128 rows] f32, columns O[0..D), frame, row sum
+// W steps cut over n CTAs: the first W mod n of them take one step more
+struct Cut {
+  int64_t q, rem;
+  __device__ __forceinline__ int64_t start(int c) const {
+    return c * q + min(static_cast<int64_t>(c), rem);
+  }
+  // the CTA that runs step t
+  __device__ __forceinline__ int of(int64_t t) const {
+    const int64_t wide = rem * (q + 1);
+    return static_cast<int>(t < wide ? div_steps(t, q + 1) : rem + div_steps(t - wide, q));
+  }
+};
+// One tile of a piece, column-major, so that a warp's 32 rows of one column are 128 contiguous
+// bytes: [D + 2 columns][128 rows] f32, columns O[0..D), frame, row sum.  (Row-major pieces, stored
+// 16 bytes a lane and row, took the 2048-token chunk at 16384 keys from 346 to 368 us.)  A CTA has
+// two slots: 0 for the piece its run begins with, 1 for one that it reaches after other units.
 template <int D>
 __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t) {
   return part + ((static_cast<int64_t>(c) * 2 + slot) * 2 + t) * (D + 2) * kBM;
+}
+
+// Merge of one unit's pieces by the 256 softmax threads.  A tile's threads (both tiles' where tile
+// B is absent) are laid out as Rp rows x column groups, Rp the rows in use rounded up to a power of
+// two: a few rows spread over many column groups.  kCols columns of kFly pieces are loaded together
+// and joined with a running frame.  A piece whose row saw no key has frame -inf.
+template <int D, bool BF16>
+__device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) {
+  constexpr int kFly = 4, kCols = 16;
+  const bool both = sg.tokB == 0;
+  const int th = threadIdx.x - 128;
+  const int t = both ? 0 : th >> 7;
+  const int u = both ? th : th & 127;
+  const int threads = both ? 256 : 128;
+  const int rows = (t ? sg.tokB : sg.tokA) * args.G;
+  int Rp = 4;
+  while (Rp < rows) Rp *= 2;
+  const int r = u & (Rp - 1);
+  if (r >= rows) return;
+  const int cols = D * Rp / threads, col0 = (u / Rp) * cols;
+  const int n = sg.c_last - sg.c_first + 1;
+  // CTA c_first's piece may lie in its second slot, the others' are in their first
+  const float* p_first = piece_tile<D>(args.part, sg.c_first, sg.slot_first, t) + r;
+  const float* p_rest = piece_tile<D>(args.part, sg.c_first, 0, t) + r;
+  const int64_t step = 4 * (D + 2) * kBM;  // floats from a CTA's slot 0 to the next CTA's
+  const int tok = r / args.G;
+  uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
+                  (sg.g * args.G + (r - tok * args.G)) * args.o_head_stride;
+#pragma unroll 1
+  for (int k0 = col0; k0 < col0 + cols; k0 += kCols) {
+    float F = -INFINITY, L = 0.f;
+    float acc[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += kFly) {
+      float f[kFly], l[kFly], v[kFly][kCols];
+#pragma unroll
+      for (int c = 0; c < kFly; ++c) {
+        const bool in = c0 + c < n;
+        const float* p = c0 + c == 0 ? p_first : p_rest + (c0 + c) * step;
+        f[c] = in ? __ldcg(p + D * kBM) : -INFINITY;
+        l[c] = in ? __ldcg(p + (D + 1) * kBM) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          v[c][i] = in && i < cols ? __ldcg(p + (k0 + i) * kBM) : 0.f;
+      }
+      const float top = fmaxf(F, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+      if (top == -INFINITY) continue;
+      const float a = ex2(F - top);  // F = -inf: 0
+      L *= a;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] *= a;
+      F = top;
+#pragma unroll
+      for (int c = 0; c < kFly; ++c) {
+        if (f[c] == -INFINITY) continue;  // its O is not a number
+        const float w = ex2(f[c] - F);
+        L = fmaf(w, l[c], L);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] = fmaf(w, v[c][i], acc[i]);
+      }
+    }
+    const float inv = F == -INFINITY ? 0.f : 1.f / L;
+    uint32_t w[kCols / 2];
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) w[i] = pack2<BF16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (cols >= kCols) {
+      reinterpret_cast<uint4*>(orow + k0 * 2)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(orow + k0 * 2)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i)
+        if (2 * i < cols) reinterpret_cast<uint32_t*>(orow + k0 * 2)[i] = w[i];
+    }
+  }
 }
 
 // Epilogue of one piece of a unit cut between CTAs, run by all softmax threads: store this row's
@@ -129,20 +216,18 @@ __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t
 // merges; every CTA that does writes the same bytes.  Both CTA-wide waits are bounded mbarriers.
 // Returns false if one gave up.
 template <int D, bool BF16>
-__device__ __noinline__ bool paged_piece(const PArgs& args, int64_t W, int n_ctas,
-                                         const PSeg* sgp, uint32_t ocol, bool active, bool valid,
-                                         float f, float l, uint32_t bar0, int pseg,
-                                         volatile int* abort_flag,
+__device__ __noinline__ bool paged_piece(const PArgs& args, const PSeg* sgp, uint32_t ocol,
+                                         bool active, bool valid, float f, float l,
+                                         uint32_t bar0, int pseg, volatile int* abort_flag,
                                          volatile uint32_t* merge_flag) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int t = (warp >= 8) ? 1 : 0;
   const int row = 32 * (warp & 3) + lane;
   const int cta = static_cast<int>(blockIdx.x);
-  const int64_t unit_start = sgp->unit_start;
-  const int slot = run_slot(cta, unit_start, W, n_ctas);
-  const int ntok = t ? sgp->tokB : sgp->tokA;
-  const int rows = ntok * args.G;  // rows of this tile in use
+  const int c_first = sgp->c_first, c_last = sgp->c_last;
+  const int slot = cta == c_first ? sgp->slot_first : 0;
+  const int rows = (t ? sgp->tokB : sgp->tokA) * args.G;  // rows of this tile in use
   if (32 * (warp & 3) < rows) {
     float* pt = piece_tile<D>(args.part, cta, slot, t) + row;
     const bool have = active && f != -INFINITY;
@@ -168,8 +253,6 @@ __device__ __noinline__ bool paged_piece(const PArgs& args, int64_t W, int n_cta
     tc_fence_before();
     mbar_arrive(bar0 + 8u * (pbOFree + t));
   }
-  const int c_first = run_of(unit_start, W, n_ctas);
-  const int c_last = run_of(unit_start + sgp->nb - 1, W, n_ctas);
   mbar_arrive(bar0 + 8u * pbPiece);
   if (warp == 4) {
     bool okw = mbar_wait(bar0 + 8u * pbPiece, pseg & 1, abort_flag, &g_prefill_paged_error);
@@ -181,7 +264,7 @@ __device__ __noinline__ bool paged_piece(const PArgs& args, int64_t W, int n_cta
       fence_sc_gpu();
       all = true;
       for (int c = c_first + lane; c <= c_last; c += 32)
-        all = all && ld_relaxed_gpu(args.pflags + 2 * c + run_slot(c, unit_start, W, n_ctas)) ==
+        all = all && ld_relaxed_gpu(args.pflags + 2 * c + (c == c_first ? sgp->slot_first : 0)) ==
                          args.tag;
       all = __all_sync(0xffffffffu, all);
       if (all) fence_acq_rel_gpu();
@@ -194,73 +277,11 @@ __device__ __noinline__ bool paged_piece(const PArgs& args, int64_t W, int n_cta
   const bool ok = mbar_wait(bar0 + 8u * pbDecided, pseg & 1, abort_flag, &g_prefill_paged_error);
   if (!__all_sync(0xffffffffu, ok)) return false;
   if (*merge_flag == 0u) return true;
-  // frame F = max over the pieces, weights 2^(f_p - F), pieces in CTA order.  Rp rows across the
-  // lanes, so that a piece's column is read as one run; the tile's 128 threads share the columns
-  // out when there are fewer rows than threads.
-  const int Rp = rows > 64 ? 128 : rows > 32 ? 64 : 32;
-  const int u = 32 * (warp & 3) + lane;
-  const int r = u % Rp, cg = u / Rp;
-  if (rows > 0 && r < rows) {
-    auto tile_of = [&](int c) -> const float* {
-      return piece_tile<D>(args.part, c, run_slot(c, unit_start, W, n_ctas), t) + r;
-    };
-    float F = -INFINITY;
-#pragma unroll 4
-    for (int c = c_first; c <= c_last; ++c) F = fmaxf(F, __ldcg(tile_of(c) + D * kBM));
-    float L = 0.f;
-#pragma unroll 4
-    for (int c = c_first; c <= c_last; ++c) {
-      const float* pc = tile_of(c);
-      const float fp = __ldcg(pc + D * kBM), lp = __ldcg(pc + (D + 1) * kBM);
-      if (fp != -INFINITY) L = fmaf(ex2(fp - F), lp, L);
-    }
-    const float inv_l = F == -INFINITY ? 0.f : 1.f / L;
-    const int tok = r / args.G;
-    uint8_t* orow = args.o + (sgp->row0 + t * args.tile_tok + tok) * args.o_row_stride +
-                    (sgp->g * args.G + (r - tok * args.G)) * args.o_head_stride;
-    const int cols = D * Rp / kBM;  // columns of this thread
-#pragma unroll 1
-    for (int c0 = cg * cols; c0 < (cg + 1) * cols; c0 += 16) {
-      float acc[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-      for (int c = c_first; c <= c_last; c += 2) {
-        // two pieces' loads in flight together
-        const bool two = c < c_last;
-        const float* p0 = tile_of(c);
-        const float* p1 = tile_of(two ? c + 1 : c);
-        const float f0 = __ldcg(p0 + D * kBM), f1 = __ldcg(p1 + D * kBM);
-        float v0[16], v1[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v0[i] = __ldcg(p0 + (c0 + i) * kBM);
-          v1[i] = __ldcg(p1 + (c0 + i) * kBM);
-        }
-        if (f0 != -INFINITY) {
-          const float w = ex2(f0 - F);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v0[i], acc[i]);
-        }
-        if (two && f1 != -INFINITY) {
-          const float w = ex2(f1 - F);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v1[i], acc[i]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pk[i] = pack2<BF16>(acc[8 * h + 2 * i] * inv_l, acc[8 * h + 2 * i + 1] * inv_l);
-        *reinterpret_cast<uint4*>(orow + (c0 + 8 * h) * 2) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      }
-    }
-  }
+  merge_pieces<D, BF16>(args, *sgp);
   if (warp == 4) {
     // clear the unit's flags for the next call (or graph replay) with this tag
     for (int c = c_first + lane; c <= c_last; c += 32)
-      st_relaxed_gpu(args.pflags + 2 * c + run_slot(c, unit_start, W, n_ctas), 0u);
+      st_relaxed_gpu(args.pflags + 2 * c + (c == c_first ? sgp->slot_first : 0), 0u);
   }
   return true;
 }
@@ -281,12 +302,10 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   uint8_t* bgen = sgen + C::kOffBar;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bgen + kOffAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bgen + kOffTmem);
-  int64_t* plan = reinterpret_cast<int64_t*>(bgen + kOffPlan);
-  PSeg* segq = reinterpret_cast<PSeg*>(bgen + kOffSegQ);
+  int64_t* run_steps = reinterpret_cast<int64_t*>(bgen + kOffPlan);
   auto seg_at = [&](int i) -> PSeg* {
     return reinterpret_cast<PSeg*>(bgen + kOffSegQ + (i % kSegQ) * 64);
   };
-  (void)segq;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -313,21 +332,43 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     return n;
   };
 
+  // warp 0 only: this CTA's run and the unit it begins with
+  Cut cut = {1, 0};
+  int n_ctas = 0;
+  int64_t t_begin = 0, t_end = 0;
+  int b = 0, tok = 0, g = 0, nb = 1;  // sequence, first token of the pair, kv head, blocks
+  int64_t u0 = 0;                     // global step of the unit's block 0
+  SeqInfo sq = {0, 0, 0};
+  const int nbox = kBN / args.box;  // boxes of a tile
+  // the page that holds keys [j * 128 + lane * box, + box) of the sequence, -1 where there are none
+  // (not checked yet: the value is not waited for here)
+  auto look_up = [&](int j) -> int {
+    const int key = j * kBN + lane * args.box;
+    if (lane >= nbox || key >= sq.len) return -1;
+    return __ldg(bt.table + static_cast<int64_t>(b) * bt.pages_per_seq + key / bt.page_size);
+  };
+  int page0 = -1;  // of the next segment's first block, looked up ahead
   if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
     // steps in all; a batch description that is not a rising run of rows makes no steps
-    int64_t W = 0;
+    int64_t W = 0, own = 0;  // own: the steps of sequence `lane` (all that a small batch needs)
     bool bad = false;
     for (int b0 = 0; b0 < bt.B; b0 += 32) {
-      const int b = b0 + lane;
-      if (b < bt.B) {
-        const int v = __ldg(bt.starts + b), next = __ldg(bt.starts + b + 1);
-        const int len = __ldg(bt.lens + b);
-        if (bad_start(v, next, bt.rows)) {
+      if (b0 + lane < bt.B) {
+        const SeqInfo s = seq_info(b0 + lane);
+        const int len = __ldg(bt.lens + b0 + lane);
+        if (bad_start(s.start, s.start + s.nq, bt.rows)) {
           bad = true;
         } else {
           if (cta == 0 && (len < 0 || len > cap))
             atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
-          W += seq_steps(seq_info(b)) * args.Hkv;
+          const int64_t n = seq_steps(s) * args.Hkv;
+          if (b0 == 0) own = n;
+          W += n;
         }
       }
     }
@@ -337,14 +378,45 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       if (cta == 0 && lane == 0) atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
       W = 0;
     }
-    if (lane == 0) {
-      // one CTA per SM, but never more than steps: a unit's merge waits for every CTA between its
-      // first and its last piece
-      const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
-      plan[0] = W;
-      plan[1] = cta < n ? run_start(cta, W, n) : W;
-      plan[2] = cta < n ? run_start(cta + 1, W, n) : W;
+    // one CTA per SM, but never more than steps: a unit's merge waits for every CTA between its
+    // first and its last piece
+    n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
+    if (cta < n_ctas) {
+      cut.q = div_steps(W, n_ctas);
+      cut.rem = W - cut.q * n_ctas;
+      t_begin = cut.start(cta);
+      t_end = cut.start(cta + 1);
+      // the unit of step t_begin
+      for (int b0 = 0;; b0 += 32) {
+        if (b0 > 0) own = seq_steps(seq_info(b0 + lane)) * args.Hkv;
+        int64_t end = own;  // inclusive scan over the lanes
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
+          if (lane >= off) end += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, u0 + end > t_begin);
+        if (past) {
+          const int who = __ffs(past) - 1;
+          u0 += __shfl_sync(0xffffffffu, end - own, who);
+          b = b0 + who;
+          break;
+        }
+        u0 += __shfl_sync(0xffffffffu, end, 31);
+        if (b0 + 32 >= bt.B) break;  // (not reached: W counts these steps)
+      }
+      sq = seq_info(b);
+      nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
+      while (tok < sq.nq && t_begin >= u0 + static_cast<int64_t>(nb) * args.Hkv) {
+        u0 += static_cast<int64_t>(nb) * args.Hkv;
+        tok += pair_tok;
+        nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
+      }
+      g = static_cast<int>(div_steps(t_begin - u0, nb));
+      u0 += static_cast<int64_t>(g) * nb;
     }
+    if (lane == 0) *run_steps = t_end - t_begin;
+    if (t_begin < t_end) page0 = look_up(static_cast<int>(t_begin - u0));
   } else if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -396,69 +468,24 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t W = plan[0], t_begin = plan[1], t_end = plan[2];
-  const int n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
+  const int64_t steps = *run_steps;
 
   // registers moved to the softmax warpgroups with a q4_0 side, as in fa_prefill.cu
   if (warp < 4 || warp >= 12) {
     if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 0) {
       // -------------------------------------------------- scheduler and producer
-      if (lane == 0) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-      }
       bool ok = true;
-      // the unit of step t_begin: sequence, first token of the pair, kv head
-      int b = 0, tok = 0, g = 0;
-      int64_t u0 = 0;  // global step of the unit's block 0
-      SeqInfo sq = {0, 0, 0};
-      int nb = 1;
-      if (t_begin < t_end) {
-        for (int b0 = 0; b0 < bt.B; b0 += 32) {
-          const int64_t own = seq_steps(seq_info(b0 + lane)) * args.Hkv;
-          int64_t end = own;  // inclusive scan over the lanes
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
-            if (lane >= off) end += x;
-          }
-          const unsigned past = __ballot_sync(0xffffffffu, u0 + end > t_begin);
-          if (past) {
-            const int who = __ffs(past) - 1;
-            u0 += __shfl_sync(0xffffffffu, end - own, who);
-            b = b0 + who;
-            break;
-          }
-          u0 += __shfl_sync(0xffffffffu, end, 31);
-        }
-        sq = seq_info(b);
-        nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
-        while (t_begin >= u0 + static_cast<int64_t>(nb) * args.Hkv) {
-          u0 += static_cast<int64_t>(nb) * args.Hkv;
-          tok += pair_tok;
-          nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
-        }
-        g = static_cast<int>((t_begin - u0) / nb);
-        u0 += static_cast<int64_t>(g) * nb;
-      }
-
       int n = 0;      // ring tiles
       int rt = 0;     // raw q4_0 tiles
       int pg = 0;     // paired ring: slots filled
       int qn = 0;     // Q loads issued
       int tails = 0;  // V tiles cleared past the sequence's end
-      const int nbox = kBN / args.box;
-      // the row of the tensor map's third dimension (page, kv head) that holds keys
-      // [j * 128 + i * box, + box) of the sequence, or -1: nothing there (TMA fills with zeros)
-      auto box_at = [&](int j, int i, int& row) -> int {
-        const int key = j * kBN + i * args.box;
-        row = 0;
-        if (i >= nbox || key >= sq.len) return -1;
-        const int lp = key / bt.page_size;
-        row = key - lp * bt.page_size;
-        const int page = __ldg(bt.table + static_cast<int64_t>(b) * bt.pages_per_seq + lp);
+      // the box that a looked-up page stands for: its first row in the page, and the tensor map's
+      // third coordinate (page, kv head), -1 where there is nothing (TMA fills with zeros)
+      auto box_row = [&](int j) -> int { return (j * kBN + lane * args.box) % bt.page_size; };
+      auto box_at = [&](int j, int page) -> int {
+        if (lane >= nbox || j * kBN + lane * args.box >= sq.len) return -1;
         if (page < 0 || page >= bt.num_pages) {
           atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
           return -1;
@@ -493,12 +520,13 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         return true;
       };
       const int di = (lane % 16) / kChunks, dc = (lane % 16) % kChunks;  // dense box and chunk
-      // one slot of the paired ring: K of block kj (if >= 0) by lanes 0-15, V of block vj by 16-31
-      auto produce_pair = [&](int kj, int vj) {
+      // one slot of the paired ring: K of block j + 1 (where `k`) by lanes 0-15, at the boxes at_k /
+      // row_k that lanes 0 .. nbox - 1 hold, V of block j (where `v`) by lanes 16-31 at at_v / row_v
+      auto produce_pair = [&](bool k, int at_k, int row_k, bool v, int j, int at_v, int row_v) {
         const bool vhalf = lane >= 16;
-        const int j = vhalf ? vj : kj;
-        int row = 0, at = -1;
-        if (j >= 0) at = box_at(j, di, row);
+        const int ak = __shfl_sync(0xffffffffu, at_k, di), av = __shfl_sync(0xffffffffu, at_v, di);
+        const int rk = __shfl_sync(0xffffffffu, row_k, di);
+        const int rv = __shfl_sync(0xffffffffu, row_v, di);
         const int p = pg % C::kSlots;
         if (lane == 0 && pg >= C::kSlots)
           ok = mbar_wait(bar(pbRingEmpty + p), ((pg / C::kSlots) - 1) & 1, abort_flag,
@@ -506,31 +534,32 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) return;
         const uint32_t dst = sbase + C::kOffRing + 2 * p * C::kTileBytes;
-        const int r0 = vj >= 0 ? tail_rows(vj) : kBN;
+        const int r0 = v ? tail_rows(j) : kBN;  // (below kBN only with k false: the last block)
         if (lane == 0) {
-          const int direct = (kj >= 0 ? 1 : 0) + (vj >= 0 && r0 == kBN ? 1 : 0);
-          if (r0 < kBN) mbar_arrive_expect_tx(bar(pbTail), C::kTileBytes);
-          if (r0 == kBN) mbar_arrive_expect_tx(bar(pbRingFull + p), direct * C::kTileBytes);
+          if (r0 < kBN)
+            mbar_arrive_expect_tx(bar(pbTail), C::kTileBytes);
+          else
+            mbar_arrive_expect_tx(bar(pbRingFull + p),
+                                  ((k ? 1 : 0) + (v ? 1 : 0)) * C::kTileBytes);
         }
         __syncwarp();
-        if (j >= 0 && di < nbox)
+        if ((vhalf ? v : k) && di < nbox)
           copy_dense(vhalf ? &tm_v : &tm_k, dst + (vhalf ? C::kTileBytes : 0),
-                     r0 < kBN ? bar(pbTail) : bar(pbRingFull + p), at, row, di, dc);
+                     r0 < kBN ? bar(pbTail) : bar(pbRingFull + p), vhalf ? av : ak,
+                     vhalf ? rv : rk, di, dc);
         if (r0 < kBN) {
-          // (kj < 0 here: the tail is in the sequence's last block)
           ok = clear_tail(dst + C::kTileBytes, r0);
           if (!ok) return;
           if (lane == 0) mbar_arrive(bar(pbRingFull + p));
         }
         ++pg;
       };
-      // one tile of the unpaired ring (a q4_0 side)
-      auto produce = [&](bool is_v, int j) {
+      // one tile of the unpaired ring (a q4_0 side), at the boxes that lanes 0 .. nbox - 1 hold
+      auto produce = [&](bool is_v, int j, int at, int row) {
         if (!ok) return;
         if (!(is_v ? VQ4 : KQ4)) {
           const int s = n % C::kStages;
-          int row = 0;
-          const int at = lane < 16 ? box_at(j, di, row) : -1;
+          const int da = __shfl_sync(0xffffffffu, at, di), dr = __shfl_sync(0xffffffffu, row, di);
           if (lane == 0 && n >= C::kStages)
             ok = mbar_wait(bar(pbRingEmpty + s), ((n / C::kStages) - 1) & 1, abort_flag,
                            &g_prefill_paged_error);
@@ -542,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
           __syncwarp();
           if (lane < 16 && di < nbox)
-            copy_dense(is_v ? &tm_v : &tm_k, dst, full, at, row, di, dc);
+            copy_dense(is_v ? &tm_v : &tm_k, dst, full, da, dr, di, dc);
           if (r0 < kBN) {
             ok = clear_tail(dst, r0);
             if (!ok) return;
@@ -550,8 +579,6 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           }
         } else if constexpr (C::kAnyQ4) {
           const int s = rt % C::kRawStages;
-          int row = 0;
-          const int at = box_at(j, lane, row);
           if (lane == 0 && rt >= C::kRawStages)
             ok = mbar_wait(bar(pbRawEmpty + s), ((rt / C::kRawStages) - 1) & 1, abort_flag,
                            &g_prefill_paged_error);
@@ -607,33 +634,61 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           s->len = sq.len;
           s->nbA = blocks_seen(sq.len, sq.nq, tok + args.tile_tok, args.causal);
           s->nbB = tokB > 0 ? nb : 0;
-          s->nb = nb;
           s->j0 = j0;
           s->j1 = j1;
-          s->unit_start = u0;
+          s->c_first = j0 > 0 ? cut.of(u0) : cta;
+          s->c_last = j1 < nb ? cut.of(u0 + nb - 1) : cta;
+          s->slot_first = cut.start(s->c_first) < u0 ? 1 : 0;
           mbar_arrive(bar(pbSegFull + sidx % kSegQ));
-          if (sidx > 0)
-            ok = mbar_wait(bar(pbQEmpty), (sidx - 1) & 1, abort_flag, &g_prefill_paged_error);
-          if (ok) {
-            const uint32_t bytes = kChunks * args.tile_tok * args.G * 128;
-            mbar_arrive_expect_tx(bar(pbQFull), (tokB > 0 ? 2 : 1) * bytes);
-            for (int ti = 0; ti < (tokB > 0 ? 2 : 1); ++ti)
-              for (int c = 0; c < kChunks; ++c)
-                tma_load_3d(sbase + C::kOffQ + ti * C::kQBytes + c * (kBM * 128), &tm_q,
-                            bar(pbQFull), c * 64, g * args.G,
-                            sq.start + tok + ti * args.tile_tok);
-            ++qn;
-          }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
+        // the segment's Q tiles, once the previous segment's last QK has read the previous ones
+        auto load_q = [&]() {
+          if (lane == 0) {
+            if (sidx > 0)
+              ok = mbar_wait(bar(pbQEmpty), (sidx - 1) & 1, abort_flag, &g_prefill_paged_error);
+            if (ok) {
+              const uint32_t bytes = kChunks * args.tile_tok * args.G * 128;
+              mbar_arrive_expect_tx(bar(pbQFull), (tokB > 0 ? 2 : 1) * bytes);
+              for (int ti = 0; ti < (tokB > 0 ? 2 : 1); ++ti)
+                for (int c = 0; c < kChunks; ++c)
+                  tma_load_3d(sbase + C::kOffQ + ti * C::kQBytes + c * (kBM * 128), &tm_q,
+                              bar(pbQFull), c * 64, g * args.G,
+                              sq.start + tok + ti * args.tile_tok);
+              ++qn;
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        };
+        // block j's boxes, and the pages of block j + 1, looked up while block j is waited for.  A
+        // later segment's first K tile goes ahead of its Q tiles: it waits for a ring slot only.
+        if (sidx == 0) load_q();
+        int at = box_at(j0, page0), row = box_row(j0);
+        int next = j0 + 1 < j1 ? look_up(j0 + 1) : -1;
         if constexpr (C::kPaired) {
-          produce_pair(j0, -1);
-          for (int j = j0; j < j1 && ok; ++j) produce_pair(j + 1 < j1 ? j + 1 : -1, j);
+          if (ok) produce_pair(true, at, row, false, 0, -1, 0);
+          if (sidx > 0 && ok) load_q();
+          for (int j = j0; j < j1 && ok; ++j) {
+            const int at_v = at, row_v = row;
+            const bool more = j + 1 < j1;
+            if (more) {
+              at = box_at(j + 1, next);
+              row = box_row(j + 1);
+              if (j + 2 < j1) next = look_up(j + 2);
+            }
+            produce_pair(more, at, row, true, j, at_v, row_v);
+          }
         } else {
           for (int j = j0; j < j1 && ok; ++j) {
-            produce(false, j);
-            produce(true, j);
+            produce(false, j, at, row);
+            if (sidx > 0 && j == j0 && ok) load_q();
+            produce(true, j, at, row);
+            if (j + 1 < j1) {
+              at = box_at(j + 1, next);
+              row = box_row(j + 1);
+              if (j + 2 < j1) next = look_up(j + 2);
+            }
           }
         }
         ++sidx;
@@ -649,6 +704,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
             }
             nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
           }
+          page0 = look_up(0);
         }
       }
       if (ok && t_begin < t_end && lane == 0) {
@@ -682,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0 && t_begin < t_end) {
+      if (lane == 0 && steps > 0) {
         constexpr uint32_t idesc_qk = make_idesc_f16(kBM, kBN, BF16, false);
         constexpr uint32_t idesc_pv = make_idesc_f16(kBM, D, BF16, true);
         bool ok = true;
@@ -832,7 +888,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         const int u = C::dq_index(warp, lane);
         const uint32_t mg = opaque_u32(BF16 ? 0x43004300u : 0x64006400u);
         bool ok = true;
-        const int64_t ntiles = 2 * (t_end - t_begin);  // K and V of every step
+        const int64_t ntiles = 2 * steps;  // K and V of every step
         int r = 0;  // raw q4_0 tiles consumed
         for (int n = 0; n < ntiles; ++n) {
           if (!((n & 1) ? VQ4 : KQ4)) continue;  // a dense tile: the producer's TMA fills it
@@ -878,7 +934,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     int od = 0;    // segments in which this tile had blocks (O-done phase)
     int pseg = 0;  // pieces published so far
     int gn = 0;    // paired ring: slots of the segments before this one
-    for (int sidx = 0; t_begin < t_end; ++sidx) {
+    for (int sidx = 0; steps > 0; ++sidx) {
       ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
                      &g_prefill_paged_error);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -934,9 +990,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         tc_fence_after();
       }
       const bool valid = rtok < ntok && row < args.G * args.tile_tok;
-      const int64_t unit_start = sp->unit_start;
-      const bool split = run_of(unit_start, W, n_ctas) != run_of(unit_start + sp->nb - 1, W, n_ctas);
-      if (!split) {
+      if (sp->c_first == sp->c_last) {  // the whole unit
         if (active) {
           if (live) {
             const bool none = f == -INFINITY;  // the row sees no key
@@ -969,8 +1023,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           mbar_arrive(bar(pbOFree + t));
         }
       } else {
-        ok = paged_piece<D, BF16>(args, W, n_ctas, sp, ocol, active, valid, f, l, bar0, pseg,
-                                  abort_flag, merge_flag);
+        ok = paged_piece<D, BF16>(args, sp, ocol, active, valid, f, l, bar0, pseg, abort_flag,
+                                  merge_flag);
         ++pseg;
         if (!ok) break;
       }
@@ -986,6 +1040,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     tmem_dealloc(tmem, kTmemCols);
   }
 }
+
+size_t flag_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * sizeof(uint32_t); }
 
 template <int D, bool BF16, bool KQ4, bool VQ4>
 cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
@@ -1010,9 +1066,9 @@ cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
   a.box = paged_prefill_box(L.batch.page_size);
   a.scale_log2 = L.scale * kLog2e;
   a.pflags = static_cast<uint32_t*>(L.workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) +
-                                    (static_cast<size_t>(L.num_sms) * 2 * sizeof(uint32_t) + 255) /
-                                        256 * 256);
+  // the pieces' columns are whole 128-byte lines: from a 256-byte boundary on
+  a.part = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(L.workspace) + flag_bytes(L.num_sms) + 255) / 256 * 256);
   a.tag = L.tag;
   kern<<<L.num_sms, C::kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, a);
   return cudaGetLastError();
@@ -1037,7 +1093,7 @@ int paged_prefill_box(int page_size) {
 // publication flags, then the partial rows: two slots of two tiles for every CTA
 size_t paged_prefill_workspace(int D, int num_sms) {
   const size_t n = static_cast<size_t>(num_sms);
-  return (n * 2 * sizeof(uint32_t) + 255) / 256 * 256 + n * 4 * (D + 2) * kBM * sizeof(float);
+  return flag_bytes(num_sms) + 255 + n * 4 * (D + 2) * kBM * sizeof(float);
 }
 
 cudaError_t paged_prefill_launch(const PagedPrefillLaunch& L, cudaStream_t stream) {
