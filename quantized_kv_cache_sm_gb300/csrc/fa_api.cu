@@ -1,5 +1,7 @@
 // C-ABI front end: argument checks, TMA descriptors, kernel dispatch, device status.
 #include <math.h>
+#include <stdio.h>
+#include <stdlib.h>
 #include <atomic>
 #include <initializer_list>
 #include <mutex>
@@ -529,6 +531,7 @@ static fa_status check_paged(const void* k_pages, const int32_t* block_table,
       (v_format != FA_KV_DENSE && v_format != FA_KV_Q4_0))
     return FA_ERR_INVALID_ARG;
   if (B > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+  if (rows > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (D % 32 || D > 65536) return FA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(page_size) * pages_per_seq > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_pages) * Hkv >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
@@ -650,6 +653,10 @@ fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pag
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (G > 128 || page_size % 16) return FA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(rows) * Hq * D >= (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  // the schedule counts steps (128-key blocks of every unit) in 32 bits
+  const int64_t max_steps = (static_cast<int64_t>(rows) / (2 * (128 / G)) + B) * Hkv *
+                            (static_cast<int64_t>(page_size) * pages_per_seq / 128 + 8);
+  if (max_steps >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   const int nsm = num_sms();
   const size_t need = paged_prefill_workspace(D, nsm);
   if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))
@@ -664,7 +671,9 @@ fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pag
   const CUtensorMapSwizzle nib_sw =
       D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
   const uint64_t blocks = static_cast<uint64_t>(num_pages) * Hkv;  // (page, kv head) blocks
-  const uint32_t box = static_cast<uint32_t>(paged_prefill_box(page_size));
+  // rows that one copy takes of a page: the largest power of two that divides pages and tiles
+  uint32_t box = 16;
+  while (box < 128 && page_size % (2 * box) == 0) box *= 2;
   const size_t scale_off = q4_scale_offset(static_cast<int64_t>(blocks) * page_size, D);
   PagedPrefillLaunch L;
   // a dimension of one row or head is never stepped along: any valid stride will do
@@ -675,6 +684,8 @@ fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pag
       !kv_map(&L.tm_k, k_pages, kq4, tdt, D, page_size, blocks, box, nib_sw) ||
       !kv_map(&L.tm_v, v_pages, vq4, tdt, D, page_size, blocks, box, nib_sw))
     return FA_ERR_CUDA;
+  L.box = static_cast<int>(box);
+  while ((1 << L.box_bits) < L.box) ++L.box_bits;
   L.batch = PagedBatch{block_table, row_starts, seq_lens,  B,
                        rows,        num_pages,  page_size, pages_per_seq};
   L.o = o;
@@ -693,6 +704,7 @@ fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pag
   L.workspace = workspace;
   L.tag = next_call_tag();
   L.num_sms = nsm;
+  { const char* e = getenv("FAOPT"); int v[4] = {32, 8, 2, 0}; if (e) sscanf(e, "%d,%d,%d,%d", v, v+1, v+2, v+3); for (int i = 0; i < 4; ++i) L.opt[i] = v[i]; }
   return paged_prefill_launch(L, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
@@ -788,7 +800,8 @@ fa_status fa_get_status(fa_stream_t stream) {
   if (a == 0xffffffffu || b == 0xffffffffu || x == 0xffffffffu || r == 0xffffffffu ||
       p == 0xffffffffu)
     return FA_ERR_CUDA;
-  if (b == kErrBadIndex || r == kErrBadIndex || p == kErrBadIndex) return FA_ERR_INVALID_ARG;
+  for (const uint32_t e : {b, r, p})
+    if (e == kErrBadIndex) return FA_ERR_INVALID_ARG;
   if (a == kErrSchedule) return FA_ERR_UNSUPPORTED;
   if (a || b || c || x || p) return FA_ERR_TIMEOUT;
   return FA_OK;

@@ -131,7 +131,8 @@ uint32_t paged_take_error();
 
 // ragged prefill over page pools (fa_prefill_paged)
 struct PagedPrefillLaunch {
-  CUtensorMap tm_q, tm_k, tm_v;  // Q tiles {64, G, tokens}; page boxes of K and V (kv_box rows)
+  CUtensorMap tm_q, tm_k, tm_v;  // Q tiles {64, G, tokens}; page boxes of K and V (box rows)
+  int box, box_bits = 0;  // box = 1 << box_bits
   PagedBatch batch;
   void* o;
   int64_t o_row_stride, o_head_stride;
@@ -143,11 +144,10 @@ struct PagedPrefillLaunch {
   void* workspace;
   uint32_t tag;
   int num_sms;
+  int opt[4];
 };
 cudaError_t paged_prefill_launch(const PagedPrefillLaunch& L, cudaStream_t stream);
 size_t paged_prefill_workspace(int D, int num_sms);
-// rows of a K or V box: the part of a page that a 128-key tile takes with one copy
-int paged_prefill_box(int page_size);
 uint32_t paged_prefill_take_error();
 
 // the explicit (non-flash) path: dequant (q4_0 sides), S = scale Q K^T (f32), softmax -> P,

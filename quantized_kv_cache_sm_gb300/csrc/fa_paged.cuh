@@ -24,4 +24,205 @@ __host__ __device__ __forceinline__ bool bad_start(int v, int next, int rows) {
   return v < 0 || next < v || next > rows;
 }
 
+// x / d for 0 <= x < 2^31 by a multiplication and a shift: with s = ceil(log2 d) and m =
+// floor(2^32 (2^s - d) / d) + 1, x / d = (mulhi(m, x) + x) >> s (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994)
+struct DivBy {
+  uint32_t d, m, s;
+  DivBy() = default;
+  explicit DivBy(uint32_t divisor) : d(divisor), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>((__umulhi(m, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >>
+                            s);
+  }
+};
+
+// ------------------------------------------------------------------------------------------
+// The ragged prefill's schedule.  A work unit is `unit_tok` consecutive new tokens of a sequence
+// for one kv head; its steps are the 128-key blocks that its last token sees, at least one.  In
+// the schedule a unit counts `over` steps more, at its beginning, for what it costs whatever its
+// length (loading its queries, storing its rows).  The counts of all units -- ordered by sequence,
+// then tokens, then kv head -- are concatenated and cut evenly over the CTAs.  Lengths live on the
+// device, so every CTA finds its own run.  Counts fit 32 bits (the host checks).
+// ------------------------------------------------------------------------------------------
+struct PagedSeq {
+  int start, nq, len;  // first packed row, new tokens, keys
+};
+
+// W counts cut over n CTAs: the first W mod n of them take one more
+struct PagedCut {
+  int q = 1, rem = 0;
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+  // the CTA that holds count t
+  __device__ __forceinline__ int of(int t) const {
+    const int wide = rem * (q + 1);
+    return t < wide ? t / (q + 1) : rem + (t - wide) / q;
+  }
+};
+
+struct PagedPlan {
+  PagedBatch bt;
+  DivBy page;         // by page_size
+  int Hkv, causal;
+  int unit_tok, over;
+  // a batch whose longest unit has at most max_whole steps is shared out in whole units; longer
+  // ones are cut anywhere, into runs of at least min_run counts (a cut costs its pieces' round
+  // trip through memory and their merge)
+  int max_whole, min_run;
+
+  __device__ __forceinline__ int cap() const { return bt.page_size * bt.pages_per_seq; }
+  __device__ __forceinline__ PagedSeq seq(int b) const {
+    PagedSeq s = {0, 0, 0};
+    if (b < bt.B) {
+      s.start = __ldg(bt.starts + b);
+      s.nq = __ldg(bt.starts + b + 1) - s.start;
+      s.len = max(0, min(__ldg(bt.lens + b), cap()));
+    }
+    return s;
+  }
+  // blocks that the tokens before tok_end see, at least one
+  __device__ __forceinline__ int blocks(const PagedSeq& s, int tok_end) const {
+    const int last = causal ? s.len - s.nq + min(tok_end, s.nq) : s.len;
+    return max(1, (max(0, min(s.len, last)) + 127) >> 7);
+  }
+  // counts of a sequence's units for one kv head
+  __device__ __forceinline__ int counts(const PagedSeq& s) const {
+    int n = 0;
+    for (int t = 0; t < s.nq; t += unit_tok) n += over + blocks(s, t + unit_tok);
+    return n;
+  }
+};
+
+// One CTA's walk through its run, by one warp (every member is the same in all lanes)
+struct PagedWalk {
+  PagedCut cut;
+  int t = 0, t_end = 0;       // the next count and the end of the run
+  int u0 = 0;                 // the unit's first count (block 0 is count u0 + over)
+  int b = 0, tok = 0, g = 0;  // the unit: sequence, first token, kv head
+  int nb = 1;                 // its blocks
+  bool whole = false;         // whole units: those whose first count lies in the run
+  PagedSeq s = {0, 0, 0};
+
+  // CTA `cta`'s run out of `grid` CTAs.  Bad starts or lengths are recorded in *err by CTA 0; bad
+  // starts leave nothing to anybody.
+  __device__ __forceinline__ void find(const PagedPlan& p, int cta, int grid, uint32_t* err,
+                                       uint32_t bad_index) {
+    const int lane = threadIdx.x & 31;
+    int W = 0, own = 0, longest = 0;  // own: the counts of sequence `lane`
+    bool bad = false;
+    for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
+      const int i = b0 + lane;
+      if (i < p.bt.B) {
+        const int v = __ldg(p.bt.starts + i), next = __ldg(p.bt.starts + i + 1);
+        const int len = __ldg(p.bt.lens + i);
+        if (bad_start(v, next, p.bt.rows)) {
+          bad = true;
+        } else {
+          if (cta == 0 && (len < 0 || len > p.cap())) atomicCAS(err, 0u, bad_index);
+          const PagedSeq q = p.seq(i);
+          const int n = p.counts(q) * p.Hkv;
+          if (b0 == 0) own = n;
+          W += n;
+          if (q.nq > 0) longest = max(longest, p.blocks(q, q.nq));
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (cta == 0 && lane == 0) atomicCAS(err, 0u, bad_index);
+      return;
+    }
+    W = __reduce_add_sync(0xffffffffu, W);
+    whole = __reduce_max_sync(0xffffffffu, longest) <= p.max_whole;
+    // (min_run >= 1: every run inside a cut unit has a step, which the unit's merge waits for)
+    const int n = min(grid, whole ? W : (W + p.min_run - 1) / p.min_run);
+    if (cta >= n) return;
+    cut.q = W / n;
+    cut.rem = W - cut.q * n;
+    t = cut.start(cta);
+    t_end = cut.start(cta + 1);
+    for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
+      if (b0 > 0) own = p.counts(p.seq(b0 + lane)) * p.Hkv;
+      int end = own;  // inclusive scan over the lanes
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, off);
+        if (lane >= off) end += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, u0 + end > t);
+      if (past) {
+        const int who = __ffs(past) - 1;
+        u0 += __shfl_sync(0xffffffffu, end - own, who);
+        b = b0 + who;
+        break;
+      }
+      u0 += __shfl_sync(0xffffffffu, end, 31);
+    }
+    s = p.seq(b);
+    nb = p.blocks(s, p.unit_tok);
+    while (tok < s.nq && t >= u0 + (p.over + nb) * p.Hkv) {
+      u0 += (p.over + nb) * p.Hkv;
+      tok += p.unit_tok;
+      nb = p.blocks(s, tok + p.unit_tok);
+    }
+    g = (t - u0) / (p.over + nb);
+    u0 += g * (p.over + nb);
+    if (whole && t > u0) next(p);
+    if (!whole && t_end <= u0 + p.over) t = t_end;  // a run that ends before the unit's block 0
+  }
+
+  // the blocks [j0, j1) of the unit that belong to the run
+  __device__ __forceinline__ int j0(const PagedPlan& p) const { return max(0, t - u0 - p.over); }
+  __device__ __forceinline__ int j1(const PagedPlan& p) const {
+    return whole ? nb : min(nb, t_end - u0 - p.over);
+  }
+  // past those; the next unit if the run has blocks of it
+  __device__ __forceinline__ void next(const PagedPlan& p) {
+    u0 += p.over + nb;
+    t = u0;
+    if (t >= t_end) return;
+    if (++g == p.Hkv) {
+      g = 0;
+      tok += p.unit_tok;
+      while (tok >= s.nq && b + 1 < p.bt.B) {
+        s = p.seq(++b);
+        tok = 0;
+      }
+      nb = p.blocks(s, tok + p.unit_tok);
+    }
+    if (!whole && t_end <= u0 + p.over) t = t_end;
+  }
+  // the CTAs of the unit's first and last block, and the first one's partial slot: 1 where it
+  // reaches the unit after others, 0 where its run begins in the unit (all other pieces' slot)
+  __device__ __forceinline__ void pieces(const PagedPlan& p, int cta, int& c_first, int& c_last,
+                                         int& slot_first) const {
+    c_first = t > u0 + p.over ? cut.of(u0 + p.over) : cta;
+    c_last = !whole && t_end < u0 + p.over + nb ? cut.of(u0 + p.over + nb - 1) : cta;
+    slot_first = cut.start(c_first) < u0 ? 1 : 0;
+  }
+  // the page that holds keys [key, ...) of the sequence, -1 where there are none (not checked: the
+  // value is not waited for here)
+  __device__ __forceinline__ int look_up(const PagedPlan& p, int key) const {
+    if (key >= s.len) return -1;
+    return __ldg(p.bt.table + static_cast<int64_t>(b) * p.bt.pages_per_seq + p.page(key));
+  }
+  // a key's row in its page
+  static __device__ __forceinline__ int page_row(const PagedPlan& p, int key) {
+    return key - p.page(key) * p.bt.page_size;
+  }
+  // the tensor map's third coordinate (page, kv head) of a looked-up page; -1, where TMA fills with
+  // zeros without reading memory, for none and for one outside the pool (recorded)
+  __device__ __forceinline__ int block_of(const PagedPlan& p, int key, int page, uint32_t* err,
+                                          uint32_t bad_index) const {
+    if (key >= s.len) return -1;
+    if (page < 0 || page >= p.bt.num_pages) {
+      atomicCAS(err, 0u, bad_index);
+      return -1;
+    }
+    return page * p.Hkv + g;
+  }
+};
+
 }  // namespace fa

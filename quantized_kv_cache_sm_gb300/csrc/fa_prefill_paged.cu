@@ -28,7 +28,7 @@
 //
 // Warp roles: as in fa_prefill.cu (0 producer and scheduler, 1 TMEM and MMA issuer, 2-3 and 12-15
 // q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B).
-#include <algorithm>
+#include <limits.h>
 
 #include "fa_internal.h"
 #include "fa_paged.cuh"
@@ -59,13 +59,16 @@ enum {
   pbTail = 37,       // a V tile that needs rows cleared has landed
   pbSegFull = 38,    // + queue slot (kSegQ)
   pbSegEmpty = 42,   // + queue slot
-  pbCount = 46
+  pbSAlt = 46,       // lone tile A: scores in, and P of, the second S buffer
+  pbPAlt = 47,
+  pbPvAlt = 48,      // lone tile A: after every PV MMA
+  pbCount = 49
 };
 constexpr int kSegQ = 4;
 constexpr int kOffTmem = pbCount * 8;
 constexpr int kOffAbort = kOffTmem + 8;
 constexpr int kOffMerge = kOffAbort + 8;
-constexpr int kOffPlan = kOffMerge + 8;  // int64: steps of this CTA's run
+constexpr int kOffPlan = kOffMerge + 8;  // int: the run has segments; raw tiles before its end
 constexpr int kOffSegQ = 512;            // the segment queue
 
 // one segment: steps [j0, j1) of a unit
@@ -83,47 +86,18 @@ struct PSeg {
 static_assert(sizeof(PSeg) <= 64 && kOffSegQ + kSegQ * 64 <= 512 + 1024, "segment queue");
 
 struct PArgs {
-  PagedBatch batch;
+  PagedPlan plan;
   uint8_t* o;
   int64_t o_row_stride, o_head_stride;  // bytes
   const uint8_t* k_scale;
   const uint8_t* v_scale;
-  int Hq, Hkv, G, tile_tok, causal, box;
+  int G, tile_tok, box, box_bits;  // box = 1 << box_bits
   float scale_log2;
   float* part;       // partial rows of units cut between CTAs, 2 slots a CTA, 2 tiles a slot
   uint32_t* pflags;  // [CTAs][2] publication flags, tagged per call
   uint32_t tag;
 };
 
-// keys that tokens up to tok_end (exclusive) of a sequence of nq new tokens and len keys see, in
-// 128-key blocks, at least one
-__host__ __device__ __forceinline__ int blocks_seen(int len, int nq, int tok_end, int causal) {
-  const int last = causal ? len - nq + min(tok_end, nq) : len;
-  return max(1, (max(0, min(len, last)) + kBN - 1) / kBN);
-}
-
-struct SeqInfo {
-  int start, nq, len;
-};
-
-// Division of step counts, which rarely pass 32 bits: a 64-bit division costs some hundred
-// instructions of the scheduling lane.
-__device__ __forceinline__ int64_t div_steps(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-// W steps cut over n CTAs: the first W mod n of them take one step more
-struct Cut {
-  int64_t q, rem;
-  __device__ __forceinline__ int64_t start(int c) const {
-    return c * q + min(static_cast<int64_t>(c), rem);
-  }
-  // the CTA that runs step t
-  __device__ __forceinline__ int of(int64_t t) const {
-    const int64_t wide = rem * (q + 1);
-    return static_cast<int>(t < wide ? div_steps(t, q + 1) : rem + div_steps(t - wide, q));
-  }
-};
 // One tile of a piece, column-major, so that a warp's 32 rows of one column are 128 contiguous
 // bytes: [D + 2 columns][128 rows] f32, columns O[0..D), frame, row sum.  (Row-major pieces, stored
 // 16 bytes a lane and row, took the 2048-token chunk at 16384 keys from 346 to 368 us.)  A CTA has
@@ -131,6 +105,13 @@ struct Cut {
 template <int D>
 __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t) {
   return part + ((static_cast<int64_t>(c) * 2 + slot) * 2 + t) * (D + 2) * kBM;
+}
+
+// 16-byte asynchronous copy of which src_bytes are read, the rest zeros
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(src_bytes)
+               : "memory");
 }
 
 // Merge of one unit's pieces by the 256 softmax threads.  A tile's threads (both tiles' where tile
@@ -294,6 +275,9 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
                          const __grid_constant__ PArgs args) {
   using C = Cfg<D, KQ4, VQ4, true>;
   constexpr int kChunks = D / 64;  // 64-element column chunks of a tile
+  // a lone tile's blocks alternate between the S buffers; not with one q4_0 side, whose ring ties
+  // K and V to even and odd stages
+  constexpr bool kAlt = KQ4 == VQ4;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -302,7 +286,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   uint8_t* bgen = sgen + C::kOffBar;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bgen + kOffAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bgen + kOffTmem);
-  int64_t* run_steps = reinterpret_cast<int64_t*>(bgen + kOffPlan);
+  volatile int* has_run = reinterpret_cast<volatile int*>(bgen + kOffPlan);
+  volatile int* raw_end = has_run + 1;
   auto seg_at = [&](int i) -> PSeg* {
     return reinterpret_cast<PSeg*>(bgen + kOffSegQ + (i % kSegQ) * 64);
   };
@@ -310,42 +295,13 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x);
-  const PagedBatch& bt = args.batch;
-  const int cap = bt.page_size * bt.pages_per_seq;
+  const PagedPlan& plan = args.plan;
 
-  // ---- the batch, as the scheduling warp reads it
-  auto seq_info = [&](int b) -> SeqInfo {
-    SeqInfo s = {0, 0, 0};
-    if (b < bt.B) {
-      s.start = __ldg(bt.starts + b);
-      s.nq = __ldg(bt.starts + b + 1) - s.start;
-      s.len = max(0, min(__ldg(bt.lens + b), cap));
-    }
-    return s;
-  };
-  const int pair_tok = 2 * args.tile_tok;
-  // steps of a sequence's units for one kv head
-  auto seq_steps = [&](const SeqInfo& s) -> int64_t {
-    int64_t n = 0;
-    for (int t = 0; t < s.nq; t += pair_tok)
-      n += blocks_seen(s.len, s.nq, t + pair_tok, args.causal);
-    return n;
-  };
-
-  // warp 0 only: this CTA's run and the unit it begins with
-  Cut cut = {1, 0};
-  int n_ctas = 0;
-  int64_t t_begin = 0, t_end = 0;
-  int b = 0, tok = 0, g = 0, nb = 1;  // sequence, first token of the pair, kv head, blocks
-  int64_t u0 = 0;                     // global step of the unit's block 0
-  SeqInfo sq = {0, 0, 0};
-  const int nbox = kBN / args.box;  // boxes of a tile
-  // the page that holds keys [j * 128 + lane * box, + box) of the sequence, -1 where there are none
-  // (not checked yet: the value is not waited for here)
+  PagedWalk w;                      // warp 0 only
+  const int nbox = kBN >> args.box_bits;  // boxes of a tile
+  // lane i < nbox looks up the page of box i of block j
   auto look_up = [&](int j) -> int {
-    const int key = j * kBN + lane * args.box;
-    if (lane >= nbox || key >= sq.len) return -1;
-    return __ldg(bt.table + static_cast<int64_t>(b) * bt.pages_per_seq + key / bt.page_size);
+    return lane < nbox ? w.look_up(plan, j * kBN + (lane << args.box_bits)) : -1;
   };
   int page0 = -1;  // of the next segment's first block, looked up ahead
   if (warp == 0) {
@@ -354,69 +310,12 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
     }
-    // steps in all; a batch description that is not a rising run of rows makes no steps
-    int64_t W = 0, own = 0;  // own: the steps of sequence `lane` (all that a small batch needs)
-    bool bad = false;
-    for (int b0 = 0; b0 < bt.B; b0 += 32) {
-      if (b0 + lane < bt.B) {
-        const SeqInfo s = seq_info(b0 + lane);
-        const int len = __ldg(bt.lens + b0 + lane);
-        if (bad_start(s.start, s.start + s.nq, bt.rows)) {
-          bad = true;
-        } else {
-          if (cta == 0 && (len < 0 || len > cap))
-            atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
-          const int64_t n = seq_steps(s) * args.Hkv;
-          if (b0 == 0) own = n;
-          W += n;
-        }
-      }
+    w.find(plan, cta, gridDim.x, &g_prefill_paged_error, kErrBadIndex);
+    if (lane == 0) {
+      *has_run = w.t < w.t_end;
+      *raw_end = INT_MAX;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-    if (__any_sync(0xffffffffu, bad)) {
-      if (cta == 0 && lane == 0) atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
-      W = 0;
-    }
-    // one CTA per SM, but never more than steps: a unit's merge waits for every CTA between its
-    // first and its last piece
-    n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), W));
-    if (cta < n_ctas) {
-      cut.q = div_steps(W, n_ctas);
-      cut.rem = W - cut.q * n_ctas;
-      t_begin = cut.start(cta);
-      t_end = cut.start(cta + 1);
-      // the unit of step t_begin
-      for (int b0 = 0;; b0 += 32) {
-        if (b0 > 0) own = seq_steps(seq_info(b0 + lane)) * args.Hkv;
-        int64_t end = own;  // inclusive scan over the lanes
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
-          if (lane >= off) end += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, u0 + end > t_begin);
-        if (past) {
-          const int who = __ffs(past) - 1;
-          u0 += __shfl_sync(0xffffffffu, end - own, who);
-          b = b0 + who;
-          break;
-        }
-        u0 += __shfl_sync(0xffffffffu, end, 31);
-        if (b0 + 32 >= bt.B) break;  // (not reached: W counts these steps)
-      }
-      sq = seq_info(b);
-      nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
-      while (tok < sq.nq && t_begin >= u0 + static_cast<int64_t>(nb) * args.Hkv) {
-        u0 += static_cast<int64_t>(nb) * args.Hkv;
-        tok += pair_tok;
-        nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
-      }
-      g = static_cast<int>(div_steps(t_begin - u0, nb));
-      u0 += static_cast<int64_t>(g) * nb;
-    }
-    if (lane == 0) *run_steps = t_end - t_begin;
-    if (t_begin < t_end) page0 = look_up(static_cast<int>(t_begin - u0));
+    if (w.t < w.t_end) page0 = look_up(w.j0(plan));
   } else if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -434,18 +333,21 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       mbar_init(bar(pbPiece), 256);
       mbar_init(bar(pbDecided), 1);
       mbar_init(bar(pbTail), 1);
+      mbar_init(bar(pbSAlt), 1);
+      mbar_init(bar(pbPAlt), 128);
+      mbar_init(bar(pbPvAlt), 1);
       for (int s = 0; s < kSegQ; ++s) {
         mbar_init(bar(pbSegFull + s), 1);
         mbar_init(bar(pbSegEmpty + s), 1 + 8);  // the issuer and the eight softmax warps
       }
       for (int s = 0; s < C::kStages; ++s) {
         const bool q4s = (C::kStages % 2 == 0) ? ((s & 1) ? VQ4 : KQ4) : (KQ4 && VQ4);
-        mbar_init(bar(pbRingFull + s), q4s ? C::kDqThreads : 1);
+        mbar_init(bar(pbRingFull + s), q4s ? C::kDqWarps : 1);
         mbar_init(bar(pbRingEmpty + s), 1);
       }
       for (int s = 0; s < C::kRawStages; ++s) {
         mbar_init(bar(pbRawFull + s), 1 + 32);  // TMA lane + 32 cp.async arrivals
-        mbar_init(bar(pbRawEmpty + s), C::kDqThreads);
+        mbar_init(bar(pbRawEmpty + s), C::kDqWarps);
       }
       *abort_flag = 0;
       fence_mbar_init();
@@ -468,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t steps = *run_steps;
+  const bool run = *has_run != 0;
 
   // registers moved to the softmax warpgroups with a q4_0 side, as in fa_prefill.cu
   if (warp < 4 || warp >= 12) {
@@ -481,16 +383,13 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       int pg = 0;     // paired ring: slots filled
       int qn = 0;     // Q loads issued
       int tails = 0;  // V tiles cleared past the sequence's end
-      // the box that a looked-up page stands for: its first row in the page, and the tensor map's
-      // third coordinate (page, kv head), -1 where there is nothing (TMA fills with zeros)
-      auto box_row = [&](int j) -> int { return (j * kBN + lane * args.box) % bt.page_size; };
+      auto box_row = [&](int j) -> int {  // first row in its page of box `lane` of block j
+        return PagedWalk::page_row(plan, j * kBN + (lane << args.box_bits));
+      };
       auto box_at = [&](int j, int page) -> int {
-        if (lane >= nbox || j * kBN + lane * args.box >= sq.len) return -1;
-        if (page < 0 || page >= bt.num_pages) {
-          atomicCAS(&g_prefill_paged_error, kErrNone, kErrBadIndex);
-          return -1;
-        }
-        return page * args.Hkv + g;
+        return lane < nbox ? w.block_of(plan, j * kBN + (lane << args.box_bits), page,
+                                        &g_prefill_paged_error, kErrBadIndex)
+                           : -1;
       };
       // dense tile boxes: lane (box, chunk) of 16 copies one box's 64 columns
       auto copy_dense = [&](const CUtensorMap* tm, uint32_t dst, uint32_t full, int at, int row,
@@ -500,14 +399,14 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       // rows [len, end of its box) of a dense V tile hold no key: clear them once the tile has
       // landed (only the last block of a sequence has such rows)
       auto tail_rows = [&](int j) -> int {  // first such row of the tile, kBN if none
-        const int r0 = sq.len - j * kBN;
-        return (r0 > 0 && r0 < kBN && r0 % args.box != 0) ? r0 : kBN;
+        const int r0 = w.s.len - j * kBN;
+        return (r0 > 0 && r0 < kBN && (r0 & (args.box - 1)) != 0) ? r0 : kBN;
       };
       auto clear_tail = [&](uint32_t stage, int r0) -> bool {
         bool w = mbar_wait(bar(pbTail), tails & 1, abort_flag, &g_prefill_paged_error);
         w = __all_sync(0xffffffffu, w);
         if (!w) return false;
-        const int r1 = (r0 + args.box - 1) / args.box * args.box;
+        const int r1 = (r0 + args.box - 1) & -args.box;
         uint8_t* p = sgen + (stage - sbase);
         for (int i = lane; i < (r1 - r0) * kChunks * 8; i += 32) {
           const int c = i / ((r1 - r0) * 8), k = i - c * ((r1 - r0) * 8);
@@ -590,23 +489,21 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           if (lane < nbox)
             tma_load_3d(dst + lane * args.box * C::kNibRow, is_v ? &tm_v : &tm_k,
                         bar(pbRawFull + s), 0, row, at);
-          // scales: one 4- or 8-byte row per key, zero past the sequence's end
+          // scales: four keys a lane (they share a box), 16 or 32 contiguous bytes, zero past the
+          // sequence's end
           const uint8_t* sp = is_v ? args.v_scale : args.k_scale;
+          const int kr = 4 * lane, i = kr >> args.box_bits;
+          const int kat = __shfl_sync(0xffffffffu, at, i);
+          const int krow = __shfl_sync(0xffffffffu, row, i) + (kr & (args.box - 1));
+          const int in = kat >= 0 ? max(0, min(4, w.s.len - j * kBN - kr)) : 0;  // keys with data
+          const uint8_t* src =
+              in > 0 ? sp + (static_cast<int64_t>(kat) * plan.bt.page_size + krow) * C::kScaleRow
+                     : sp;
+          const uint32_t d = dst + C::kRawNib + kr * C::kScaleRow;
 #pragma unroll
-          for (int k = 0; k < kBN / 32; ++k) {
-            const int kr = lane + 32 * k;
-            const int i = kr / args.box;
-            const int kat = __shfl_sync(0xffffffffu, at, i);
-            const int krow = __shfl_sync(0xffffffffu, row, i) + (kr - i * args.box);
-            const bool in = kat >= 0 && j * kBN + kr < sq.len;
-            const uint8_t* src =
-                sp + (in ? (static_cast<int64_t>(kat) * bt.page_size + krow) * C::kScaleRow : 0);
-            const uint32_t d = dst + C::kRawNib + kr * C::kScaleRow;
-            if (C::kScaleRow == 8)
-              cp_async_8(d, src, in ? 8u : 0u);
-            else
-              cp_async_4(d, src, in ? 4u : 0u);
-          }
+          for (int c = 0; c < C::kScaleRow / 4; ++c)
+            cp_async_16(d + 16 * c, src + (in > 0 ? 16 * c : 0),
+                        static_cast<uint32_t>(max(0, min(16, in * C::kScaleRow - 16 * c))));
           cp_async_mbar_arrive_noinc(bar(pbRawFull + s));
           ++rt;
         }
@@ -614,31 +511,27 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       };
 
       int sidx = 0;
-      int64_t t = t_begin;
-      while (t < t_end && ok) {
-        // the unit (b, tok, g), nb steps from u0: its segment of this run
-        const int tokA = min(args.tile_tok, sq.nq - tok);
-        const int tokB = max(0, min(args.tile_tok, sq.nq - tok - args.tile_tok));
-        const int j0 = static_cast<int>(t - u0);
-        const int j1 = static_cast<int>(min(static_cast<int64_t>(nb), t_end - u0));
+      for (; w.t < w.t_end && ok; ++sidx) {
+        // the unit's segment of this run
+        const int tokA = min(args.tile_tok, w.s.nq - w.tok);
+        const int tokB = max(0, min(args.tile_tok, w.s.nq - w.tok - args.tile_tok));
+        const int j0 = w.j0(plan), j1 = w.j1(plan);
         if (lane == 0 && sidx >= kSegQ)
           ok = mbar_wait(bar(pbSegEmpty + sidx % kSegQ), ((sidx / kSegQ) - 1) & 1, abort_flag,
                          &g_prefill_paged_error);
         if (lane == 0 && ok) {
           PSeg* s = seg_at(sidx);
-          s->row0 = sq.start + tok;
-          s->g = g;
+          s->row0 = w.s.start + w.tok;
+          s->g = w.g;
           s->tokA = tokA;
           s->tokB = tokB;
-          s->pos0 = sq.len - sq.nq + tok;
-          s->len = sq.len;
-          s->nbA = blocks_seen(sq.len, sq.nq, tok + args.tile_tok, args.causal);
-          s->nbB = tokB > 0 ? nb : 0;
+          s->pos0 = w.s.len - w.s.nq + w.tok;
+          s->len = w.s.len;
+          s->nbA = plan.blocks(w.s, w.tok + args.tile_tok);
+          s->nbB = tokB > 0 ? w.nb : 0;
           s->j0 = j0;
           s->j1 = j1;
-          s->c_first = j0 > 0 ? cut.of(u0) : cta;
-          s->c_last = j1 < nb ? cut.of(u0 + nb - 1) : cta;
-          s->slot_first = cut.start(s->c_first) < u0 ? 1 : 0;
+          w.pieces(plan, cta, s->c_first, s->c_last, s->slot_first);
           mbar_arrive(bar(pbSegFull + sidx % kSegQ));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -654,8 +547,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
               for (int ti = 0; ti < (tokB > 0 ? 2 : 1); ++ti)
                 for (int c = 0; c < kChunks; ++c)
                   tma_load_3d(sbase + C::kOffQ + ti * C::kQBytes + c * (kBM * 128), &tm_q,
-                              bar(pbQFull), c * 64, g * args.G,
-                              sq.start + tok + ti * args.tile_tok);
+                              bar(pbQFull), c * 64, w.g * args.G,
+                              w.s.start + w.tok + ti * args.tile_tok);
               ++qn;
             }
           }
@@ -680,34 +573,26 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
             produce_pair(more, at, row, true, j, at_v, row_v);
           }
         } else {
+          // K0 V0 K1 V1 ..., or, where a lone tile's blocks alternate, K0 K1 V0 K2 V1 ...
+          const bool ahead = kAlt && tokB == 0;
+          produce(false, j0, at, row);
+          if (sidx > 0 && ok) load_q();
           for (int j = j0; j < j1 && ok; ++j) {
-            produce(false, j, at, row);
-            if (sidx > 0 && j == j0 && ok) load_q();
-            produce(true, j, at, row);
+            const int at_v = at, row_v = row;
+            if (!ahead) produce(true, j, at_v, row_v);
             if (j + 1 < j1) {
               at = box_at(j + 1, next);
               row = box_row(j + 1);
               if (j + 2 < j1) next = look_up(j + 2);
+              produce(false, j + 1, at, row);
             }
+            if (ahead) produce(true, j, at_v, row_v);
           }
         }
-        ++sidx;
-        t = u0 + j1;
-        if (t < t_end) {  // the next unit
-          u0 += nb;
-          if (++g == args.Hkv) {
-            g = 0;
-            tok += pair_tok;
-            while (tok >= sq.nq && b + 1 < bt.B) {
-              sq = seq_info(++b);
-              tok = 0;
-            }
-            nb = blocks_seen(sq.len, sq.nq, tok + pair_tok, args.causal);
-          }
-          page0 = look_up(0);
-        }
+        w.next(plan);
+        if (w.t < w.t_end) page0 = look_up(0);
       }
-      if (ok && t_begin < t_end && lane == 0) {
+      if (ok && run && lane == 0) {
         // end of the run
         if (sidx >= kSegQ)
           ok = mbar_wait(bar(pbSegEmpty + sidx % kSegQ), ((sidx / kSegQ) - 1) & 1, abort_flag,
@@ -715,6 +600,22 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         if (ok) {
           seg_at(sidx)->j1 = -1;
           mbar_arrive(bar(pbSegFull + sidx % kSegQ));
+        }
+      }
+      if constexpr (C::kAnyQ4) {
+        // the dequant warps learn of the end as of one more raw tile
+        if (ok && run) {
+          const int s = rt % C::kRawStages;
+          if (lane == 0 && rt >= C::kRawStages)
+            ok = mbar_wait(bar(pbRawEmpty + s), ((rt / C::kRawStages) - 1) & 1, abort_flag,
+                           &g_prefill_paged_error);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (lane == 0) {
+            *raw_end = rt;
+            if (ok) mbar_arrive(bar(pbRawFull + s));
+          }
+          __syncwarp();
+          if (ok) mbar_arrive(bar(pbRawFull + s));
         }
       }
       if (!ok && lane == 0) {
@@ -738,12 +639,12 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0 && steps > 0) {
+      if (lane == 0 && run) {
         constexpr uint32_t idesc_qk = make_idesc_f16(kBM, kBN, BF16, false);
         constexpr uint32_t idesc_pv = make_idesc_f16(kBM, D, BF16, true);
         bool ok = true;
         int n = 0, gn = 0;       // ring tiles / paired slots taken
-        int prA = 0, prB = 0;    // P-ready waits per tile before this segment (barrier phases)
+        int prA = 0, prB = 0, prAlt = 0;  // P-ready waits before this segment (barrier phases)
         int actA = 0, actB = 0;  // earlier segments in which the tile had blocks
         auto acquire_g = [&]() -> int {
           const int p = gn % C::kSlots;
@@ -762,16 +663,17 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           return s;
         };
         auto release = [&](int s) { mma_commit(bar(pbRingEmpty + s)); };
-        auto issue_qk = [&](int t, int s) {
+        // QK of tile t into S buffer sb (its own, or either for a lone tile A)
+        auto issue_qk = [&](int t, int s, int sb, int full) {
           const uint32_t qaddr = sbase + C::kOffQ + t * C::kQBytes;
           const uint32_t kaddr = sbase + C::kOffRing + s * C::kTileBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (kBM * 128) + (kk & 3) * 32;
-            mma_ss(tmem + col_s(t), make_sdesc_sw128(qaddr + off, 16, 1024),
+            mma_ss(tmem + col_s(sb), make_sdesc_sw128(qaddr + off, 16, 1024),
                    make_sdesc_sw128(kaddr + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
           }
-          mma_commit(bar(pbSFull + t));
+          mma_commit(bar(full));
         };
         auto issue_pv = [&](int t, int j, int s, int j0, int e_t, int pb) {
           ok = ok && mbar_wait(bar(pbPReady + t), (pb + j) & 1, abort_flag,
@@ -796,18 +698,70 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           const int j0 = sp->j0, j1 = sp->j1;
           if (j1 < 0) break;
           const int eA = min(j1, sp->nbA), eB = min(j1, sp->nbB);
+          const bool sp_lone = sp->tokB == 0;
           mbar_arrive(bar(pbSegEmpty + sidx % kSegQ));
           ok = mbar_wait(bar(pbQFull), sidx & 1, abort_flag, &g_prefill_paged_error);
           tc_fence_after();
           if (!ok) break;
           const int pbA = prA - j0, pbB = prB - j0;
+          if (kAlt && sp_lone) {
+            // a lone tile A: its blocks alternate between the two S buffers, so that QK(j + 1) is
+            // done while the softmax is at block j: QK(j0) QK(j0+1) | PV(j) QK(j+2) | ...
+            auto take = [&]() -> int {  // the next K (paired ring: with the V before it)
+              return C::kPaired ? 2 * acquire_g() : acquire();
+            };
+            auto qk = [&](int j, int s) {
+              const int sb = (j - j0) & 1;
+              issue_qk(0, s, sb, sb ? pbSAlt : pbSFull);
+              if (j + 1 == j1) mma_commit(bar(pbQEmpty));
+            };
+            int s = take();
+            if (!ok) break;
+            qk(j0, s);
+            release(C::kPaired ? s / 2 : s);
+            if (C::kPaired || j0 + 1 < j1) {
+              s = take();  // paired: V(j0) and K(j0 + 1)
+              if (!ok) break;
+              if (j0 + 1 < j1) qk(j0 + 1, s);
+              if (!C::kPaired) release(s);
+            }
+            if (actA > 0)
+              ok = ok && mbar_wait(bar(pbOFree + 0), (actA - 1) & 1, abort_flag,
+                                   &g_prefill_paged_error);
+            for (int j = j0; j < j1 && ok; ++j) {
+              const int sb = (j - j0) & 1;
+              if (!C::kPaired) s = acquire();
+              ok = ok && mbar_wait(bar(sb ? pbPAlt : pbPReady), (sb ? prAlt++ : prA++) & 1,
+                                   abort_flag, &g_prefill_paged_error);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t vaddr =
+                  sbase + C::kOffRing + (C::kPaired ? s + 1 : s) * C::kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_ts(tmem + C::kColO0, tmem + col_s(sb) + kk * 8,
+                       make_sdesc_sw128(vaddr + kk * (16 * 128), kBN * 128, 1024), idesc_pv,
+                       (j > j0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar(pbPvAlt));
+              if (j == j1 - 1) mma_commit(bar(pbODone));
+              release(C::kPaired ? s / 2 : s);
+              if (C::kPaired ? j + 1 < j1 : j + 2 < j1) {
+                s = take();
+                if (!ok) break;
+                if (j + 2 < j1) qk(j + 2, s);
+                if (!C::kPaired) release(s);
+              }
+            }
+            ++actA;
+            continue;
+          }
           if constexpr (C::kPaired) {
             {
               const int p = acquire_g();
               if (!ok) break;
-              if (j0 < eA) issue_qk(0, 2 * p);
+              if (j0 < eA) issue_qk(0, 2 * p, 0, pbSFull);
               if (j0 < eB)
-                issue_qk(1, 2 * p);  // tile B's softmax releases the slot
+                issue_qk(1, 2 * p, 1, pbSFull + 1);  // tile B's softmax releases the slot
               else
                 release(p);
               if (j0 + 1 == j1) mma_commit(bar(pbQEmpty));
@@ -824,11 +778,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
               if (!ok) break;
               if (j < eA) issue_pv(0, j, 2 * p + 1, j0, eA, pbA);
               if (!ok) break;
-              if (next && j + 1 < eA) issue_qk(0, 2 * p);
+              if (next && j + 1 < eA) issue_qk(0, 2 * p, 0, pbSFull);
               if (j < eB) issue_pv(1, j, 2 * p + 1, j0, eB, pbB);
               if (!ok) break;
               if (next && j + 1 < eB)
-                issue_qk(1, 2 * p);
+                issue_qk(1, 2 * p, 1, pbSFull + 1);
               else
                 release(p);
               if (next && j + 2 == j1) mma_commit(bar(pbQEmpty));
@@ -837,8 +791,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
             {
               const int sK = acquire();
               if (!ok) break;
-              if (j0 < eA) issue_qk(0, sK);
-              if (j0 < eB) issue_qk(1, sK);
+              if (j0 < eA) issue_qk(0, sK, 0, pbSFull);
+              if (j0 < eB) issue_qk(1, sK, 1, pbSFull + 1);
               release(sK);
               if (j0 + 1 == j1) mma_commit(bar(pbQEmpty));
             }
@@ -855,12 +809,12 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
               if (!ok) break;
               if (j < eA) issue_pv(0, j, sV, j0, eA, pbA);
               if (!ok) break;
-              if (next && j + 1 < eA) issue_qk(0, sK);
+              if (next && j + 1 < eA) issue_qk(0, sK, 0, pbSFull);
               if (j < eB) issue_pv(1, j, sV, j0, eB, pbB);
               if (!ok) break;
               release(sV);
               if (next) {
-                if (j + 1 < eB) issue_qk(1, sK);
+                if (j + 1 < eB) issue_qk(1, sK, 1, pbSFull + 1);
                 release(sK);
                 if (j + 2 == j1) mma_commit(bar(pbQEmpty));
               }
@@ -888,15 +842,15 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         const int u = C::dq_index(warp, lane);
         const uint32_t mg = opaque_u32(BF16 ? 0x43004300u : 0x64006400u);
         bool ok = true;
-        const int64_t ntiles = 2 * steps;  // K and V of every step
         int r = 0;  // raw q4_0 tiles consumed
-        for (int n = 0; n < ntiles; ++n) {
+        for (int n = 0; run; ++n) {
           if (!((n & 1) ? VQ4 : KQ4)) continue;  // a dense tile: the producer's TMA fills it
           const int rs = r % C::kRawStages;
           const int s = n % C::kStages;
           ok = mbar_wait(bar(pbRawFull + rs), (r / C::kRawStages) & 1, abort_flag,
                          &g_prefill_paged_error);
-          if (ok && n >= C::kStages)
+          if (!ok || r >= *raw_end) break;
+          if (n >= C::kStages)
             ok = mbar_wait(bar(pbRingEmpty + s), ((n / C::kStages) - 1) & 1, abort_flag,
                            &g_prefill_paged_error);
           if (!ok) break;
@@ -912,8 +866,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           }
           // generic-proxy writes must be visible to the tensor core's async proxy
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          mbar_arrive(bar(pbRingFull + s));
-          mbar_arrive(bar(pbRawEmpty + rs));
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(pbRingFull + s));
+            mbar_arrive(bar(pbRawEmpty + rs));
+          }
           ++r;
         }
       }
@@ -931,10 +888,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(bgen + kOffMerge);
     bool ok = true;
     int sf = 0;    // S-full waits so far (barrier phase)
+    int sf_alt = 0, pv_alt = 0;  // lone tile A: those of the second S buffer, and its PVs so far
     int od = 0;    // segments in which this tile had blocks (O-done phase)
     int pseg = 0;  // pieces published so far
     int gn = 0;    // paired ring: slots of the segments before this one
-    for (int sidx = 0; steps > 0; ++sidx) {
+    for (int sidx = 0; run; ++sidx) {
       ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
                      &g_prefill_paged_error);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -949,16 +907,18 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       const int len = sp->len;
       const int first_pos = sp->pos0 + t * args.tile_tok;  // of the tile's first token
       // last key that this row sees, and the last one that every row of the tile sees
-      const int lim = args.causal ? min(len - 1, first_pos + rtok) : len - 1;
-      const int lim_all = args.causal ? min(len - 1, first_pos) : len - 1;
+      const int lim = plan.causal ? min(len - 1, first_pos + rtok) : len - 1;
+      const int lim_all = plan.causal ? min(len - 1, first_pos) : len - 1;
       const bool live = 32 * (warp & 3) < ntok * args.G;  // some row of the warp is in use
       float f = -INFINITY;  // frame, base-2 units of the scaled score
       float l = 0.f;
       int nres = 0;
       float pmx = 0.f;
+      const bool lone = kAlt && sp->tokB == 0;  // (tile B's warps have no blocks then)
       for (int j = j0; j < e_t; ++j) {
-        ok = mbar_wait(bar(pbSFull + t), sf & 1, abort_flag, &g_prefill_paged_error);
-        ++sf;
+        const bool second = lone && ((j - j0) & 1);
+        ok = mbar_wait(bar(second ? pbSAlt : pbSFull + t), (second ? sf_alt++ : sf++) & 1,
+                       abort_flag, &g_prefill_paged_error);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -971,15 +931,26 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         }
         if (live) {
           const int kb = j * kBN;
-          softmax_block<D, BF16>(scol, ocol, kb + kBN - 1 > lim_all, lim - kb, sl2, j > j0, f, l,
-                                 nres, pmx);
+          // a lone tile's PV(j - 1) may still be adding to O when this block moves the frame; PV(j)
+          // cannot have started, so the PVs done are those up to j - 2 or j - 1
+          auto wait_pv = [&]() {
+            if (lone) {
+              mbar_wait(bar(pbPvAlt), (pv_alt + j - j0 - 1) & 1, abort_flag,
+                        &g_prefill_paged_error);
+              tc_fence_after();
+            }
+          };
+          softmax_block<D, BF16>(second ? tmem + lane_off + col_s(1) : scol, ocol,
+                                 kb + kBN - 1 > lim_all, lim - kb, sl2, j > j0, f, l, nres, pmx,
+                                 wait_pv);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(bar(pbPReady + t));
+        mbar_arrive(bar(second ? pbPAlt : pbPReady + t));
       }
       if (!ok) break;
       const bool active = e_t > j0;  // the tile had key blocks in this segment
+      if (lone && active) pv_alt += j1 - j0;
       if (active) {
         ok = mbar_wait(bar(pbODone + t), od & 1, abort_flag, &g_prefill_paged_error);
         ++od;
@@ -1052,18 +1023,17 @@ cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
                                              C::kSmemBytes);
   if (e != cudaSuccess) return e;
   PArgs a;
-  a.batch = L.batch;
   a.o = static_cast<uint8_t*>(L.o);
   a.o_row_stride = 2 * L.o_row_stride;
   a.o_head_stride = 2 * L.o_head_stride;
   a.k_scale = static_cast<const uint8_t*>(L.k_scale);
   a.v_scale = static_cast<const uint8_t*>(L.v_scale);
-  a.Hq = L.Hq;
-  a.Hkv = L.Hkv;
   a.G = L.Hq / L.Hkv;
   a.tile_tok = kBM / a.G;
-  a.causal = L.causal;
-  a.box = paged_prefill_box(L.batch.page_size);
+  a.plan = PagedPlan{L.batch, DivBy(L.batch.page_size), L.Hkv, L.causal, 2 * a.tile_tok, L.opt[2],
+                     L.opt[0], L.opt[1]};
+  a.box = L.box;
+  a.box_bits = L.box_bits;
   a.scale_log2 = L.scale * kLog2e;
   a.pflags = static_cast<uint32_t*>(L.workspace);
   // the pieces' columns are whole 128-byte lines: from a 256-byte boundary on
@@ -1083,12 +1053,6 @@ cudaError_t launch_fmt(const PagedPrefillLaunch& L, cudaStream_t stream) {
 }
 
 }  // namespace
-
-int paged_prefill_box(int page_size) {
-  int box = 16;
-  while (box < kBN && page_size % (2 * box) == 0) box *= 2;
-  return box;
-}
 
 // publication flags, then the partial rows: two slots of two tiles for every CTA
 size_t paged_prefill_workspace(int D, int num_sms) {
