@@ -54,21 +54,24 @@ enum {
   pbRawEmpty = 28,   // + raw stage
   pbQEmpty = 32,     // the segment's last QK MMA has read the Q tiles
   pbOFree = 33,      // + tile (2): the segment's epilogue has read O out of TMEM
-  pbPiece = 35,      // all 256 softmax threads have stored their rows of a piece
-  pbDecided = 36,    // the piece's flag is published and the merge decision made
   pbTail = 37,       // a V tile that needs rows cleared has landed
   pbSegFull = 38,    // + queue slot (kSegQ)
   pbSegEmpty = 42,   // + queue slot
   pbSAlt = 46,       // lone tile A: scores in, and P of, the second S buffer
   pbPAlt = 47,
   pbPvAlt = 48,      // lone tile A: after every PV MMA
-  pbCount = 49
+  // a run cuts two units at most: that of its first segment (+ 0), which others began, and that of
+  // its last (+ 1), which others go on with
+  pbPiece = 49,      // all 256 softmax threads have stored their rows of the piece
+  pbDecided = 51,    // whether all pieces were there is decided
+  pbEarly = 53,      // the last: whether all others are there before its own is stored
+  pbCount = 54
 };
 constexpr int kSegQ = 4;
 constexpr int kOffTmem = pbCount * 8;
 constexpr int kOffAbort = kOffTmem + 8;
-constexpr int kOffMerge = kOffAbort + 8;
-constexpr int kOffPlan = kOffMerge + 8;  // int: the run has segments; raw tiles before its end
+constexpr int kOffMerge = kOffAbort + 8;  // decisions: first piece, last piece, last piece early
+constexpr int kOffPlan = kOffMerge + 16;  // int: the run has segments; raw tiles before its end
 constexpr int kOffSegQ = 512;            // the segment queue
 
 // one segment: steps [j0, j1) of a unit
@@ -83,7 +86,9 @@ struct PSeg {
   int c_first, c_last;  // CTAs of the unit's first and last step (equal: not cut)
   int slot_first;       // partial slot of the first one's piece (the others' is 0)
 };
-static_assert(sizeof(PSeg) <= 64 && kOffSegQ + kSegQ * 64 <= 512 + 1024, "segment queue");
+constexpr int kOffFirst = kOffSegQ + kSegQ * 64;  // the first segment, kept for its merge
+static_assert(sizeof(PSeg) <= 64 && kOffFirst + 64 <= 512 + 1024, "segment queue");
+static_assert(kOffPlan + 8 <= kOffSegQ, "barrier area");
 
 struct PArgs {
   PagedPlan plan;
@@ -105,6 +110,43 @@ struct PArgs {
 template <int D>
 __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t) {
   return part + ((static_cast<int64_t>(c) * 2 + slot) * 2 + t) * (D + 2) * kBM;
+}
+
+// the thread's number, formed anew where it is asked for
+__device__ __forceinline__ int opaque_tid() {
+  uint32_t tid;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+  return static_cast<int>(tid);
+}
+// mbar_wait with the abort flag at a shared address (no generic pointer kept in registers)
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (lds32(abort_at)) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      asm volatile("st.volatile.shared.b32 [%0], 1;" ::"r"(abort_at) : "memory");
+      atomicCAS(&g_prefill_paged_error, kErrNone, kErrTimeout);
+      return false;
+    }
+  }
+}
+// 16 columns of this thread's TMEM row
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {  // as reg_fence32
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 // 16-byte asynchronous copy of which src_bytes are read, the rest zeros
@@ -168,8 +210,8 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
       F = top;
 #pragma unroll
       for (int c = 0; c < kFly; ++c) {
-        if (f[c] == -INFINITY) continue;  // its O is not a number
-        const float w = ex2(f[c] - F);
+        const float w = f[c] == -INFINITY ? 0.f : ex2(f[c] - F);
+        if (w == 0.f) continue;  // (frame -inf: its O is not a number)
         L = fmaf(w, l[c], L);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) acc[i] = fmaf(w, v[c][i], acc[i]);
@@ -190,81 +232,130 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
   }
 }
 
-// Epilogue of one piece of a unit cut between CTAs, run by all softmax threads: store this row's
-// (O, frame, row sum), release O, publish the piece's flag, and merge all pieces if this CTA finds
-// them all published.  Of two pieces published at the same time at least one sees the other's flag
-// (release store, then a sequentially consistent fence before the flag loads), so at least one CTA
-// merges; every CTA that does writes the same bytes.  Both CTA-wide waits are bounded mbarriers.
-// Returns false if one gave up.
+// The same for at most kFewPieces pieces and a thread's own row, whose own piece is still in tensor
+// memory, 16 columns at a time.  The pieces are joined in CTA order with the arithmetic of
+// merge_pieces, so that the result does not depend on which CTA came last.
+constexpr int kFewPieces = 3;
 template <int D, bool BF16>
-__device__ __noinline__ bool paged_piece(const PArgs& args, const PSeg* sgp, uint32_t ocol,
-                                         bool active, bool valid, float f, float l,
-                                         uint32_t bar0, int pseg, volatile int* abort_flag,
-                                         volatile uint32_t* merge_flag) {
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const int t = (warp >= 8) ? 1 : 0;
-  const int row = 32 * (warp & 3) + lane;
-  const int cta = static_cast<int>(blockIdx.x);
-  const int c_first = sgp->c_first, c_last = sgp->c_last;
-  const int slot = cta == c_first ? sgp->slot_first : 0;
-  const int rows = (t ? sgp->tokB : sgp->tokA) * args.G;  // rows of this tile in use
-  if (32 * (warp & 3) < rows) {
-    float* pt = piece_tile<D>(args.part, cta, slot, t) + row;
-    const bool have = active && f != -INFINITY;
-    if (active) {
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(ocol + 32 * c, r);
-        tmem_wait_ld();
-        reg_fence32(r);
-        if (valid) {
+__device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg, int t, int row,
+                                               uint32_t ocol, bool active, bool valid, float f,
+                                               float l) {
+  const int64_t step = 4 * (D + 2) * kBM;  // floats from a CTA's slot 0 to the next CTA's
+  const float* p_first = piece_tile<D>(args.part, sg.c_first, sg.slot_first, t) + row;
+  const float* p_rest = piece_tile<D>(args.part, sg.c_first, 0, t) + row;
+  const int n = sg.c_last - sg.c_first + 1, own = static_cast<int>(blockIdx.x) - sg.c_first;
+  float w[kFewPieces], lc[kFewPieces];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) pt[(32 * c + i) * kBM] = __uint_as_float(r[i]);
-        }
+  for (int c = 0; c < kFewPieces; ++c) {
+    const bool in = valid && c < n && c != own;
+    const float* p = c == 0 ? p_first : p_rest + c * step;
+    w[c] = in ? __ldcg(p + D * kBM) : -INFINITY;
+    lc[c] = in ? __ldcg(p + (D + 1) * kBM) : 0.f;
+    if (c == own && active) {
+      w[c] = f;
+      lc[c] = l;
+    }
+  }
+  const float F = fmaxf(w[0], fmaxf(w[1], w[2]));
+  float L = 0.f;
+#pragma unroll
+  for (int c = 0; c < kFewPieces; ++c) {
+    w[c] = w[c] == -INFINITY ? 0.f : ex2(w[c] - F);  // 0: the piece's O is not a number
+    if (w[c] != 0.f) L = fmaf(w[c], lc[c], L);
+  }
+  const float inv = F == -INFINITY ? 0.f : 1.f / L;
+  const int tok = row / args.G;
+  uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
+                  (sg.g * args.G + (row - tok * args.G)) * args.o_head_stride;
+#pragma unroll 1
+  for (int k = 0; k < D; k += 16) {
+    uint32_t r[16];
+    if (active) {
+      tmem_ld16(ocol + k, r);
+      tmem_wait_ld();
+      reg_fence16(r);
+    }
+    if (!valid) continue;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kFewPieces; ++c) {
+      if (w[c] == 0.f) continue;
+      const float* p = (c == 0 ? p_first : p_rest + c * step) + k * kBM;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = c == own ? __uint_as_float(r[i]) : __ldcg(p + i * kBM);
+        acc[i] = fmaf(w[c], v, acc[i]);
       }
     }
-    if (valid) {
-      pt[D * kBM] = have ? f : -INFINITY;
-      pt[(D + 1) * kBM] = have ? l : 0.f;
-    }
+    uint32_t pk[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    reinterpret_cast<uint4*>(orow + 2 * k)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    reinterpret_cast<uint4*>(orow + 2 * k)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
   }
+}
+
+// Publication flag of CTA c's piece
+__device__ __forceinline__ uint32_t* piece_flag(const PArgs& args, const PSeg& sg, int c) {
+  return args.pflags + 2 * c + (c == sg.c_first ? sg.slot_first : 0);
+}
+// whether all pieces but CTA `but`'s (-1: all pieces) are published, by one warp; their rows may be
+// read after it
+__device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, int but) {
+  bool all = true;
+  for (int c = sg.c_first + (threadIdx.x & 31); c <= sg.c_last; c += 32)
+    all = all && (c == but || ld_relaxed_gpu(piece_flag(args, sg, c)) == args.tag);
+  all = __all_sync(0xffffffffu, all);
+  if (all) fence_acq_rel_gpu();
+  return all;
+}
+
+// Store of a thread's row of a piece
+template <int D>
+__device__ __forceinline__ void store_piece(const PArgs& args, const PSeg& sg, int t, int row,
+                                            uint32_t ocol, bool active, bool valid, float f,
+                                            float l) {
+  const int cta = static_cast<int>(blockIdx.x);
+  float* pt = piece_tile<D>(args.part, cta, cta == sg.c_first ? sg.slot_first : 0, t) + row;
+  const bool have = active && f != -INFINITY;
   if (active) {
-    tc_fence_before();
-    mbar_arrive(bar0 + 8u * (pbOFree + t));
-  }
-  mbar_arrive(bar0 + 8u * pbPiece);
-  if (warp == 4) {
-    bool okw = mbar_wait(bar0 + 8u * pbPiece, pseg & 1, abort_flag, &g_prefill_paged_error);
-    okw = __all_sync(0xffffffffu, okw);
-    bool all = false;
-    if (okw) {
-      if (lane == 0) st_release_gpu(args.pflags + 2 * cta + slot, args.tag);
-      __syncwarp();
-      fence_sc_gpu();
-      all = true;
-      for (int c = c_first + lane; c <= c_last; c += 32)
-        all = all && ld_relaxed_gpu(args.pflags + 2 * c + (c == c_first ? sgp->slot_first : 0)) ==
-                         args.tag;
-      all = __all_sync(0xffffffffu, all);
-      if (all) fence_acq_rel_gpu();
-    }
-    if (lane == 0) {
-      *merge_flag = all ? 1u : 0u;
-      mbar_arrive(bar0 + 8u * pbDecided);
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t r[32];
+      tmem_ld32(ocol + 32 * c, r);
+      tmem_wait_ld();
+      reg_fence32(r);
+      if (valid) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pt[(32 * c + i) * kBM] = __uint_as_float(r[i]);
+      }
     }
   }
-  const bool ok = mbar_wait(bar0 + 8u * pbDecided, pseg & 1, abort_flag, &g_prefill_paged_error);
-  if (!__all_sync(0xffffffffu, ok)) return false;
-  if (*merge_flag == 0u) return true;
-  merge_pieces<D, BF16>(args, *sgp);
-  if (warp == 4) {
-    // clear the unit's flags for the next call (or graph replay) with this tag
-    for (int c = c_first + lane; c <= c_last; c += 32)
-      st_relaxed_gpu(args.pflags + 2 * c + (c == c_first ? sgp->slot_first : 0), 0u);
+  if (valid) {
+    pt[D * kBM] = have ? f : -INFINITY;
+    pt[(D + 1) * kBM] = have ? l : 0.f;
   }
-  return true;
+}
+
+// Publication of this CTA's piece by one warp, once all rows are stored; whether all pieces are there
+// by then.  Of two pieces published at the same time at least one sees the other's flag (release
+// store, then a sequentially consistent fence before the flag loads), so at least one CTA finds
+// them all and merges; every CTA that does writes the same bytes.
+__device__ __forceinline__ bool publish_piece(const PArgs& args, const PSeg& sg, uint32_t stored,
+                                              uint32_t stop) {
+  if (!__all_sync(0xffffffffu, wait_bounded(stored, 0, stop))) return false;
+  if ((threadIdx.x & 31) == 0)
+    st_release_gpu(piece_flag(args, sg, static_cast<int>(blockIdx.x)), args.tag);
+  __syncwarp();
+  fence_sc_gpu();
+  return pieces_there(args, sg, -1);
+}
+// for the next call (or graph replay) with this tag
+__device__ __forceinline__ void clear_flags(const PArgs& args, const PSeg& sg) {
+  for (int c = sg.c_first + (threadIdx.x & 31); c <= sg.c_last; c += 32)
+    st_relaxed_gpu(piece_flag(args, sg, c), 0u);
 }
 
 template <int D, bool BF16, bool KQ4, bool VQ4>
@@ -330,12 +421,15 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
       mbar_init(bar(pbDrain), 1);
       mbar_init(bar(pbQEmpty), 1);
-      mbar_init(bar(pbPiece), 256);
-      mbar_init(bar(pbDecided), 1);
       mbar_init(bar(pbTail), 1);
       mbar_init(bar(pbSAlt), 1);
       mbar_init(bar(pbPAlt), 128);
       mbar_init(bar(pbPvAlt), 1);
+      mbar_init(bar(pbEarly), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(pbPiece + i), 256);
+        mbar_init(bar(pbDecided + i), 1);
+      }
       for (int s = 0; s < kSegQ; ++s) {
         mbar_init(bar(pbSegFull + s), 1);
         mbar_init(bar(pbSegEmpty + s), 1 + 8);  // the issuer and the eight softmax warps
@@ -878,129 +972,219 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   } else {
     if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
     // ---------------------------------------------------------------- softmax rows
-    const int t = (warp >= 8) ? 1 : 0;  // query tile
-    const int row = 32 * (warp & 3) + lane;
-    const int rtok = row / args.G;      // this row's token within the tile
-    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t scol = tmem + lane_off + col_s(t);
-    const uint32_t ocol = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
-    const float sl2 = args.scale_log2;
-    volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(bgen + kOffMerge);
-    bool ok = true;
-    int sf = 0;    // S-full waits so far (barrier phase)
-    int sf_alt = 0, pv_alt = 0;  // lone tile A: those of the second S buffer, and its PVs so far
-    int od = 0;    // segments in which this tile had blocks (O-done phase)
-    int pseg = 0;  // pieces published so far
-    int gn = 0;    // paired ring: slots of the segments before this one
-    for (int sidx = 0; run; ++sidx) {
-      ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
-                     &g_prefill_paged_error);
+    // Registers: a block's 128 scores and little else.  Nothing but the two words below is carried
+    // from one segment to the next, and what follows from the thread's number or the segment is
+    // formed again where it is used: values kept across the block loop, or across the call that
+    // ends a cut segment, would be spilled inside it (measured: 343 -> 383 us on the 2048-token
+    // chunk at 16384 keys).
+    enum : uint32_t {
+      kPhS = 1,       // barrier phases: S-full,
+      kPhAlt = 2,     // S-full of the second buffer,
+      kPhPv = 4,      // PVs of a lone tile,
+      kPhO = 8,       // O-done
+      kLone = 16,     // the segment: its tile is alone (its blocks alternate),
+      kLive = 32,     // some row of the warp is in use,
+      kLater = 64,    // O holds earlier blocks,
+      kSecond = 128,  // the block uses the second buffer,
+      kTileB = 256,
+      kFirstCut = 512  // the run's first segment was a piece
+    };
+    uint32_t st = 0;
+    int ks = 0;  // paired ring: the slot that holds the block's K
+    const uint32_t stop = bar0 + kOffAbort;
+    volatile uint32_t* decisions = reinterpret_cast<volatile uint32_t*>(bgen + kOffMerge);
+    bool open = false;    // the loop was left with a segment whose rows are still in tensor memory
+    int sidx = 0;
+    uint32_t tm = 0;      // this warp's TMEM lanes
+    float f = -INFINITY;  // frame, base-2 units of the scaled score
+    float l = 0.f;
+    for (; run; ++sidx) {
+      bool ok = wait_bounded(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, stop);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const PSeg* sp = seg_at(sidx);
-      const int j1 = sp->j1;
-      if (j1 < 0) break;
-      const int j0 = sp->j0;
-      const int g0 = gn - j0;  // ring slot of the one holding K(j): g0 + j
-      gn += j1 - j0 + 1;
-      const int ntok = t ? sp->tokB : sp->tokA;
-      const int e_t = ntok > 0 ? min(j1, t ? sp->nbB : sp->nbA) : 0;
-      const int len = sp->len;
-      const int first_pos = sp->pos0 + t * args.tile_tok;  // of the tile's first token
-      // last key that this row sees, and the last one that every row of the tile sees
-      const int lim = plan.causal ? min(len - 1, first_pos + rtok) : len - 1;
-      const int lim_all = plan.causal ? min(len - 1, first_pos) : len - 1;
-      const bool live = 32 * (warp & 3) < ntok * args.G;  // some row of the warp is in use
-      float f = -INFINITY;  // frame, base-2 units of the scaled score
-      float l = 0.f;
-      int nres = 0;
-      float pmx = 0.f;
-      const bool lone = kAlt && sp->tokB == 0;  // (tile B's warps have no blocks then)
-      for (int j = j0; j < e_t; ++j) {
-        const bool second = lone && ((j - j0) & 1);
-        ok = mbar_wait(bar(second ? pbSAlt : pbSFull + t), (second ? sf_alt++ : sf++) & 1,
-                       abort_flag, &g_prefill_paged_error);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+      int left;      // blocks of this tile still to come
+      int rel;       // last key that this thread's row sees, relative to the block
+      f = -INFINITY;
+      l = 0.f;
+      {
+        const PSeg* sp = seg_at(sidx);
+        const int j0 = sp->j0, j1 = sp->j1;
+        if (j1 < 0) break;
+        const int tid = opaque_tid();
+        const int t = tid >= 256 ? 1 : 0, row = tid & 127;
+        const int ntok = t ? sp->tokB : sp->tokA;
+        left = ntok > 0 ? max(0, min(j1, t ? sp->nbB : sp->nbA) - j0) : 0;
+        const int last = sp->len - 1;
+        rel = (plan.causal ? min(last, sp->pos0 + t * args.tile_tok + row / args.G) : last) -
+              j0 * kBN;
+        st = (st & (kPhS | kPhAlt | kPhPv | kPhO | kFirstCut)) | (t ? kTileB : 0) |
+             ((row & ~31) < ntok * args.G ? kLive : 0) | (kAlt && sp->tokB == 0 ? kLone : 0);
+        tm = *reinterpret_cast<volatile uint32_t*>(tmem_slot) +
+             (static_cast<uint32_t>(row & ~31) << 16);
+      }
+      for (; left > 0; --left) {
+        const int t = st & kTileB ? 1 : 0;
+        ok = wait_bounded(bar(st & kSecond ? pbSAlt : pbSFull + t),
+                          st & kSecond ? (st >> 1) & 1 : st & 1, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        st ^= st & kSecond ? kPhAlt : kPhS;
         tc_fence_after();
         if constexpr (C::kPaired) {
-          // QK_B of block j done: release the ring slot holding K(j)
-          if (t == 1 && warp == 8 && lane == 0)
-            mbar_arrive(bar(pbRingEmpty + (g0 + j) % C::kSlots));
+          // QK_B of the block done: release the ring slot holding its K
+          if (opaque_tid() == 256) mbar_arrive(bar(pbRingEmpty + ks));
+          if (++ks == C::kSlots) ks = 0;
         }
-        if (live) {
-          const int kb = j * kBN;
-          // a lone tile's PV(j - 1) may still be adding to O when this block moves the frame; PV(j)
-          // cannot have started, so the PVs done are those up to j - 2 or j - 1
+        if (st & kLive) {
+          // a lone tile's PV of the block before may still be adding to O when this block moves the
+          // frame; its own PV cannot have started, so the PVs done are all but one or all
           auto wait_pv = [&]() {
-            if (lone) {
-              mbar_wait(bar(pbPvAlt), (pv_alt + j - j0 - 1) & 1, abort_flag,
-                        &g_prefill_paged_error);
+            if (st & kLone) {
+              wait_bounded(bar(pbPvAlt), ((st >> 2) & 1) ^ 1, stop);
               tc_fence_after();
             }
           };
-          softmax_block<D, BF16>(second ? tmem + lane_off + col_s(1) : scol, ocol,
-                                 kb + kBN - 1 > lim_all, lim - kb, sl2, j > j0, f, l, nres, pmx,
-                                 wait_pv);
+          int moves = 0;
+          float top = 0.f;
+          softmax_block<D, BF16>(tm + (st & (kSecond | kTileB) ? col_s(1) : col_s(0)),
+                                 tm + (st & kTileB ? C::kColO1 : C::kColO0),
+                                 __any_sync(0xffffffffu, rel < kBN - 1), rel, args.scale_log2,
+                                 (st & kLater) != 0, f, l, moves, top, wait_pv);
           tmem_wait_st();
         }
+        rel -= kBN;
         tc_fence_before();
-        mbar_arrive(bar(second ? pbPAlt : pbPReady + t));
+        mbar_arrive(bar(st & kSecond ? pbPAlt : pbPReady + (st & kTileB ? 1 : 0)));
+        st |= kLater;
+        if (st & kLone) st ^= kSecond | kPhPv;
       }
       if (!ok) break;
-      const bool active = e_t > j0;  // the tile had key blocks in this segment
-      if (lone && active) pv_alt += j1 - j0;
-      if (active) {
-        ok = mbar_wait(bar(pbODone + t), od & 1, abort_flag, &g_prefill_paged_error);
-        ++od;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+      open = true;
+      const PSeg* sp = seg_at(sidx);
+      const int tid = opaque_tid();
+      const int t = tid >= 256 ? 1 : 0, row = tid & 127;  // query tile, this thread's row
+      const int rtok = row / args.G;                      // the row's token within the tile
+      const int ntok = t ? sp->tokB : sp->tokA;
+      const uint32_t ocol = tm + (t ? C::kColO1 : C::kColO0);
+      if constexpr (C::kPaired) {
+        const int j0 = sp->j0, j1 = sp->j1;
+        const int n = ntok > 0 ? max(0, min(j1, t ? sp->nbB : sp->nbA) - j0) : 0;
+        ks = (ks + j1 - j0 - n + 1) % C::kSlots;
+      }
+      if (sp->c_last != cta) break;  // the run ends inside the unit: below
+      const bool cut = sp->c_first != cta;
+      if (st & kLater) {  // the tile had key blocks in this segment
+        ok = wait_bounded(bar(pbODone + t), (st >> 3) & 1, stop);
+        st ^= kPhO;
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       }
       const bool valid = rtok < ntok && row < args.G * args.tile_tok;
-      if (sp->c_first == sp->c_last) {  // the whole unit
-        if (active) {
-          if (live) {
-            const bool none = f == -INFINITY;  // the row sees no key
-            const float inv_l = 1.f / l;
-            uint8_t* orow =
-                args.o + (sp->row0 + t * args.tile_tok + rtok) * args.o_row_stride +
-                (sp->g * args.G + (row - rtok * args.G)) * args.o_head_stride;
+      if (cut) {  // the last piece of a unit that other CTAs began
+        if (st & kLive) store_piece<D>(args, *sp, t, row, ocol, (st & kLater) != 0, valid, f, l);
+      } else if ((st & kLater) && (st & kLive)) {
+        const bool none = f == -INFINITY;  // the row sees no key
+        const float inv_l = 1.f / l;
+        uint8_t* orow = args.o + (sp->row0 + t * args.tile_tok + rtok) * args.o_row_stride +
+                        (sp->g * args.G + (row - rtok * args.G)) * args.o_head_stride;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(ocol + 32 * c, r);
-              tmem_wait_ld();
-              reg_fence32(r);
-              uint32_t pk[16];
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(ocol + 32 * c, r);
+          tmem_wait_ld();
+          reg_fence32(r);
+          uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                pk[i] = none ? 0u
-                             : pack2<BF16>(__uint_as_float(r[2 * i]) * inv_l,
-                                           __uint_as_float(r[2 * i + 1]) * inv_l);
-              if (valid) {
-                uint4* dst = reinterpret_cast<uint4*>(orow + c * 64);
+          for (int i = 0; i < 16; ++i)
+            pk[i] = none ? 0u
+                         : pack2<BF16>(__uint_as_float(r[2 * i]) * inv_l,
+                                       __uint_as_float(r[2 * i + 1]) * inv_l);
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 64);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-              }
-            }
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           }
-          // O has been read out of tensor memory: the next segment's PV may overwrite it
-          tc_fence_before();
-          mbar_arrive(bar(pbOFree + t));
         }
-      } else {
-        ok = paged_piece<D, BF16>(args, sp, ocol, active, valid, f, l, bar0, pseg, abort_flag,
-                                  merge_flag);
-        ++pseg;
-        if (!ok) break;
+      }
+      if (st & kLater) {
+        // O has been read out of tensor memory: the next segment's PV may overwrite it
+        tc_fence_before();
+        mbar_arrive(bar(pbOFree + t));
+      }
+      if (cut) {
+        // published at once; if the others were there before it, its merge waits for the run's end
+        mbar_arrive(bar(pbPiece));
+        if (tid < 160) {
+          const bool all = publish_piece(args, *sp, bar(pbPiece), stop);
+          if (lane == 0) {
+            *reinterpret_cast<PSeg*>(bgen + kOffFirst) = *sp;
+            decisions[0] = all ? 1u : 0u;
+            mbar_arrive(bar(pbDecided));
+          }
+        }
+        st |= kFirstCut;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(pbSegEmpty + sidx % kSegQ));
+      open = false;
+    }
+    // The run's last segment, if others go on with its unit.  Where all their pieces are published by
+    // now, nobody else can merge: this CTA does, without publishing its own -- from tensor memory
+    // where the pieces are few.  Else the piece is stored and published, and merged if all are
+    // there then.
+    if (open && run) {
+      const PSeg& sg = *seg_at(sidx);
+      const int t = warp >= 8 ? 1 : 0, row = threadIdx.x & 127;
+      const int ntok = t ? sg.tokB : sg.tokA;
+      const bool active = (st & kLater) != 0;
+      const bool valid = row / args.G < ntok && row < args.G * args.tile_tok;
+      const uint32_t ocol = tm + (t ? C::kColO1 : C::kColO0);
+      bool ok = true;
+      if (warp == 4) {
+        const bool early = pieces_there(args, sg, cta);
+        if (lane == 0) {
+          decisions[2] = early ? 1u : 0u;
+          mbar_arrive(bar(pbEarly));
+        }
+      }
+      if (active) {
+        ok = wait_bounded(bar(pbODone + t), (st >> 3) & 1, stop);
+        tc_fence_after();
+      }
+      ok = wait_bounded(bar(pbEarly), 0, stop) && ok;
+      if (__all_sync(0xffffffffu, ok)) {
+        const bool early = decisions[2] != 0u;
+        if (early && sg.c_last - sg.c_first < kFewPieces) {
+          if (st & kLive)
+            merge_with_own<D, BF16>(args, sg, t, row, ocol, active, valid, f, l);
+          if (warp == 4) clear_flags(args, sg);
+        } else {
+          if (st & kLive) store_piece<D>(args, sg, t, row, ocol, active, valid, f, l);
+          mbar_arrive(bar(pbPiece + 1));
+          if (warp == 4) {
+            const bool all = early ? __all_sync(0xffffffffu, wait_bounded(bar(pbPiece + 1), 0, stop))
+                                   : publish_piece(args, sg, bar(pbPiece + 1), stop);
+            if (lane == 0) {
+              decisions[1] = all ? 1u : 0u;
+              mbar_arrive(bar(pbDecided + 1));
+            }
+          }
+          ok = wait_bounded(bar(pbDecided + 1), 0, stop);
+          if (__all_sync(0xffffffffu, ok) && decisions[1] != 0u) {
+            merge_pieces<D, BF16>(args, sg);
+            if (warp == 4) clear_flags(args, sg);
+          }
+        }
+      }
+    }
+    // the first segment's unit, if its other pieces were there before this CTA's
+    if (st & kFirstCut) {
+      const bool ok = wait_bounded(bar(pbDecided), 0, stop);
+      if (__all_sync(0xffffffffu, ok) && decisions[0] != 0u) {
+        const PSeg& sg = *reinterpret_cast<const PSeg*>(bgen + kOffFirst);
+        merge_pieces<D, BF16>(args, sg);
+        if (warp == 4) clear_flags(args, sg);
+      }
     }
   }
 
