@@ -1,7 +1,5 @@
 // C-ABI front end: argument checks, TMA descriptors, kernel dispatch, device status.
 #include <math.h>
-#include <stdio.h>
-#include <stdlib.h>
 #include <atomic>
 #include <initializer_list>
 #include <mutex>
@@ -704,7 +702,6 @@ fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pag
   L.workspace = workspace;
   L.tag = next_call_tag();
   L.num_sms = nsm;
-  { const char* e = getenv("FAOPT"); int v[4] = {32, 8, 2, 0}; if (e) sscanf(e, "%d,%d,%d,%d", v, v+1, v+2, v+3); for (int i = 0; i < 4; ++i) L.opt[i] = v[i]; }
   return paged_prefill_launch(L, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

@@ -144,7 +144,6 @@ struct PagedPrefillLaunch {
   void* workspace;
   uint32_t tag;
   int num_sms;
-  int opt[4];
 };
 cudaError_t paged_prefill_launch(const PagedPrefillLaunch& L, cudaStream_t stream);
 size_t paged_prefill_workspace(int D, int num_sms);

@@ -67,11 +67,18 @@ struct PagedPlan {
   PagedBatch bt;
   DivBy page;         // by page_size
   int Hkv, causal;
-  int unit_tok, over;
-  // a batch whose longest unit has at most max_whole steps is shared out in whole units; longer
-  // ones are cut anywhere, into runs of at least min_run counts (a cut costs its pieces' round
-  // trip through memory and their merge)
-  int max_whole, min_run;
+  int unit_tok;
+  // A unit's start and end (first scores, last products, epilogue) count as two of its blocks.  (1,
+  // 2 or 4: the same within 1 % from one token a sequence to the 2048-token chunk; 0 leaves runs of
+  // many short units late.)
+  static constexpr int kOver = 2;
+  // A cut costs its pieces' round trip through memory and their merge: units of up to so many blocks
+  // stay whole (a run's end inside one moves to the nearer end of it), longer ones are cut anywhere.
+  // Measured, D = 64, f16 K and q4_0 V, prompts of up to 1000 tokens: 19.2 us with 8 or 16, 20.8
+  // with 0 or 4; 16 sequences of mixed lengths, bf16 at D = 128: 52.5 us with 0 or 8, 67.0 with 16.
+  // A limit of 32 for units of one 32-row quarter of a tile alone took 16 sequences of a few q4_0
+  // draft tokens from 48.0 to 45.8 us, and the mixed batch from 52.5 to 58.5.
+  static constexpr int kWhole = 8;
 
   __device__ __forceinline__ int cap() const { return bt.page_size * bt.pages_per_seq; }
   __device__ __forceinline__ PagedSeq seq(int b) const {
@@ -91,7 +98,7 @@ struct PagedPlan {
   // counts of a sequence's units for one kv head
   __device__ __forceinline__ int counts(const PagedSeq& s) const {
     int n = 0;
-    for (int t = 0; t < s.nq; t += unit_tok) n += over + blocks(s, t + unit_tok);
+    for (int t = 0; t < s.nq; t += unit_tok) n += kOver + blocks(s, t + unit_tok);
     return n;
   }
 };
@@ -103,7 +110,7 @@ struct PagedWalk {
   int u0 = 0;                 // the unit's first count (block 0 is count u0 + over)
   int b = 0, tok = 0, g = 0;  // the unit: sequence, first token, kv head
   int nb = 1;                 // its blocks
-  bool whole = false;         // whole units: those whose first count lies in the run
+  bool whole = false;         // the unit is not cut
   PagedSeq s = {0, 0, 0};
 
   // CTA `cta`'s run out of `grid` CTAs.  Bad starts or lengths are recorded in *err by CTA 0; bad
@@ -111,7 +118,7 @@ struct PagedWalk {
   __device__ __forceinline__ void find(const PagedPlan& p, int cta, int grid, uint32_t* err,
                                        uint32_t bad_index) {
     const int lane = threadIdx.x & 31;
-    int W = 0, own = 0, longest = 0;  // own: the counts of sequence `lane`
+    int W = 0, own = 0;  // own: the counts of sequence `lane`
     bool bad = false;
     for (int b0 = 0; b0 < p.bt.B; b0 += 32) {
       const int i = b0 + lane;
@@ -122,11 +129,9 @@ struct PagedWalk {
           bad = true;
         } else {
           if (cta == 0 && (len < 0 || len > p.cap())) atomicCAS(err, 0u, bad_index);
-          const PagedSeq q = p.seq(i);
-          const int n = p.counts(q) * p.Hkv;
+          const int n = p.counts(p.seq(i)) * p.Hkv;
           if (b0 == 0) own = n;
           W += n;
-          if (q.nq > 0) longest = max(longest, p.blocks(q, q.nq));
         }
       }
     }
@@ -135,9 +140,7 @@ struct PagedWalk {
       return;
     }
     W = __reduce_add_sync(0xffffffffu, W);
-    whole = __reduce_max_sync(0xffffffffu, longest) <= p.max_whole;
-    // (min_run >= 1: every run inside a cut unit has a step, which the unit's merge waits for)
-    const int n = min(grid, whole ? W : (W + p.min_run - 1) / p.min_run);
+    const int n = min(grid, W);
     if (cta >= n) return;
     cut.q = W / n;
     cut.rem = W - cut.q * n;
@@ -162,25 +165,40 @@ struct PagedWalk {
     }
     s = p.seq(b);
     nb = p.blocks(s, p.unit_tok);
-    while (tok < s.nq && t >= u0 + (p.over + nb) * p.Hkv) {
-      u0 += (p.over + nb) * p.Hkv;
+    while (tok < s.nq && t >= u0 + (p.kOver + nb) * p.Hkv) {
+      u0 += (p.kOver + nb) * p.Hkv;
       tok += p.unit_tok;
       nb = p.blocks(s, tok + p.unit_tok);
     }
-    g = (t - u0) / (p.over + nb);
-    u0 += g * (p.over + nb);
-    if (whole && t > u0) next(p);
-    if (!whole && t_end <= u0 + p.over) t = t_end;  // a run that ends before the unit's block 0
+    g = (t - u0) / (p.kOver + nb);
+    u0 += g * (p.kOver + nb);
+    settle(p);
+    if (whole && t > u0) {
+      if (2 * (t - u0) >= p.kOver + nb) {
+        next(p);
+        return;
+      }
+      t = u0;
+    }
+    stop_before(p);
+  }
+  __device__ __forceinline__ void settle(const PagedPlan& p) {
+    whole = nb <= p.kWhole;
+  }
+  // ends the run at a unit that it has no blocks of: it ends before block 0, or in the first half of
+  // a unit that is not cut
+  __device__ __forceinline__ void stop_before(const PagedPlan& p) {
+    if (whole ? 2 * (t_end - u0) < p.kOver + nb : t_end <= u0 + p.kOver) t = t_end;
   }
 
   // the blocks [j0, j1) of the unit that belong to the run
-  __device__ __forceinline__ int j0(const PagedPlan& p) const { return max(0, t - u0 - p.over); }
+  __device__ __forceinline__ int j0(const PagedPlan& p) const { return max(0, t - u0 - p.kOver); }
   __device__ __forceinline__ int j1(const PagedPlan& p) const {
-    return whole ? nb : min(nb, t_end - u0 - p.over);
+    return whole ? nb : min(nb, t_end - u0 - p.kOver);
   }
   // past those; the next unit if the run has blocks of it
   __device__ __forceinline__ void next(const PagedPlan& p) {
-    u0 += p.over + nb;
+    u0 += p.kOver + nb;
     t = u0;
     if (t >= t_end) return;
     if (++g == p.Hkv) {
@@ -191,15 +209,16 @@ struct PagedWalk {
         tok = 0;
       }
       nb = p.blocks(s, tok + p.unit_tok);
+      settle(p);
     }
-    if (!whole && t_end <= u0 + p.over) t = t_end;
+    stop_before(p);
   }
   // the CTAs of the unit's first and last block, and the first one's partial slot: 1 where it
   // reaches the unit after others, 0 where its run begins in the unit (all other pieces' slot)
   __device__ __forceinline__ void pieces(const PagedPlan& p, int cta, int& c_first, int& c_last,
                                          int& slot_first) const {
-    c_first = t > u0 + p.over ? cut.of(u0 + p.over) : cta;
-    c_last = !whole && t_end < u0 + p.over + nb ? cut.of(u0 + p.over + nb - 1) : cta;
+    c_first = t > u0 + p.kOver ? cut.of(u0 + p.kOver) : cta;
+    c_last = !whole && t_end < u0 + p.kOver + nb ? cut.of(u0 + p.kOver + nb - 1) : cta;
     slot_first = cut.start(c_first) < u0 ? 1 : 0;
   }
   // the page that holds keys [key, ...) of the sequence, -1 where there are none (not checked: the

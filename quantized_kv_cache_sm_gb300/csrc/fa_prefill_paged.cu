@@ -16,8 +16,8 @@
 //  * A work unit is a pair of consecutive tiles (A, B) of one sequence and kv head; its steps are
 //    the 128-key blocks that the pair sees, at least one.  All units' steps are concatenated
 //    (sequence, then pair, then kv head) and cut evenly over one CTA per SM, whatever the mix of
-//    long chunks and single tokens; a unit cut between CTAs is merged by the piece that finds all
-//    its siblings published.  Lengths live on the device, so every CTA finds its own run: one warp
+//    long chunks and single tokens (short units stay whole, see PagedPlan); a unit cut between CTAs
+//    is merged by the piece that finds all its siblings published.  Lengths live on the device, so every CTA finds its own run: one warp
 //    sums the steps of the batch, locates the run and feeds the other roles one segment (a run of
 //    steps of one unit) at a time through a small queue in shared memory.
 //  * A 128-key tile is fetched as 128 / box boxes of box = gcd(page_size, 128) keys, each with its
@@ -85,6 +85,7 @@ struct PSeg {
   int j0, j1;     // j1 = -1: no more segments
   int c_first, c_last;  // CTAs of the unit's first and last step (equal: not cut)
   int slot_first;       // partial slot of the first one's piece (the others' is 0)
+  int own_slot;         // and of this CTA's
 };
 constexpr int kOffFirst = kOffSegQ + kSegQ * 64;  // the first segment, kept for its merge
 static_assert(sizeof(PSeg) <= 64 && kOffFirst + 64 <= 512 + 1024, "segment queue");
@@ -132,23 +133,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
     }
   }
 }
-// 16 columns of this thread's TMEM row
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {  // as reg_fence32
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
 // 16-byte asynchronous copy of which src_bytes are read, the rest zeros
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -169,7 +153,7 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
   const int u = both ? th : th & 127;
   const int threads = both ? 256 : 128;
   const int rows = (t ? sg.tokB : sg.tokA) * args.G;
-  int Rp = 4;
+  int Rp = 512 / D;  // (at least two columns a thread)
   while (Rp < rows) Rp *= 2;
   const int r = u & (Rp - 1);
   if (r >= rows) return;
@@ -233,7 +217,7 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
 }
 
 // The same for at most kFewPieces pieces and a thread's own row, whose own piece is still in tensor
-// memory, 16 columns at a time.  The pieces are joined in CTA order with the arithmetic of
+// memory, 32 columns at a time.  The pieces are joined in CTA order with the arithmetic of
 // merge_pieces, so that the result does not depend on which CTA came last.
 constexpr int kFewPieces = 3;
 template <int D, bool BF16>
@@ -268,32 +252,46 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
   uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
                   (sg.g * args.G + (row - tok * args.G)) * args.o_head_stride;
 #pragma unroll 1
-  for (int k = 0; k < D; k += 16) {
-    uint32_t r[16];
+  for (int k = 0; k < D; k += 32) {
+    uint32_t r[32];
+    __syncwarp();  // the loads from tensor memory are the whole warp's
     if (active) {
-      tmem_ld16(ocol + k, r);
+      tmem_ld32(ocol + k, r);
       tmem_wait_ld();
-      reg_fence16(r);
+      reg_fence32(r);
     }
     if (!valid) continue;
-    float acc[16];
+    float v[kFewPieces - 1][32];  // the other pieces' columns, all loads in flight together
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int x = 0; x < kFewPieces - 1; ++x) {
+      const int c = x < own ? x : x + 1;
+      const float* p = (c == 0 ? p_first : p_rest + c * step) + k * kBM;
+      if (c < n) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[x][i] = __ldcg(p + i * kBM);
+      }
+    }
+    float acc[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int c = 0; c < kFewPieces; ++c) {
       if (w[c] == 0.f) continue;
-      const float* p = (c == 0 ? p_first : p_rest + c * step) + k * kBM;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = c == own ? __uint_as_float(r[i]) : __ldcg(p + i * kBM);
-        acc[i] = fmaf(w[c], v, acc[i]);
+      for (int i = 0; i < 32; ++i) {
+        const float x = c == own                                ? __uint_as_float(r[i])
+                        : c == 0 || (c == 1 && own == 0)        ? v[0][i]
+                                                                : v[1][i];
+        acc[i] = fmaf(w[c], x, acc[i]);
       }
     }
-    uint32_t pk[8];
+    uint32_t pk[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    reinterpret_cast<uint4*>(orow + 2 * k)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    reinterpret_cast<uint4*>(orow + 2 * k)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(orow + 2 * k)[i] =
+          make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
   }
 }
 
@@ -312,18 +310,20 @@ __device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, 
   return all;
 }
 
-// Store of a thread's row of a piece
+// Store of a thread's row of a piece into one of the CTA's slots.  (The slot is passed in, not
+// selected here by `cta == sg.c_first ? sg.slot_first : 0`: in the build whose softmax warps take
+// registers over, that conditional load gave now and then 512 for 0, a warp at a time.)
 template <int D>
-__device__ __forceinline__ void store_piece(const PArgs& args, const PSeg& sg, int t, int row,
+__device__ __forceinline__ void store_piece(const PArgs& args, int slot, int t, int row,
                                             uint32_t ocol, bool active, bool valid, float f,
                                             float l) {
-  const int cta = static_cast<int>(blockIdx.x);
-  float* pt = piece_tile<D>(args.part, cta, cta == sg.c_first ? sg.slot_first : 0, t) + row;
+  float* pt = piece_tile<D>(args.part, static_cast<int>(blockIdx.x), slot, t) + row;
   const bool have = active && f != -INFINITY;
   if (active) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t r[32];
+      __syncwarp();
       tmem_ld32(ocol + 32 * c, r);
       tmem_wait_ld();
       reg_fence32(r);
@@ -347,7 +347,7 @@ __device__ __forceinline__ bool publish_piece(const PArgs& args, const PSeg& sg,
                                               uint32_t stop) {
   if (!__all_sync(0xffffffffu, wait_bounded(stored, 0, stop))) return false;
   if ((threadIdx.x & 31) == 0)
-    st_release_gpu(piece_flag(args, sg, static_cast<int>(blockIdx.x)), args.tag);
+    st_release_gpu(args.pflags + 2 * static_cast<int>(blockIdx.x) + sg.own_slot, args.tag);
   __syncwarp();
   fence_sc_gpu();
   return pieces_there(args, sg, -1);
@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           s->j0 = j0;
           s->j1 = j1;
           w.pieces(plan, cta, s->c_first, s->c_last, s->slot_first);
+          s->own_slot = s->c_first == cta ? s->slot_first : 0;
           mbar_arrive(bar(pbSegFull + sidx % kSegQ));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -1080,7 +1081,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
       const bool valid = rtok < ntok && row < args.G * args.tile_tok;
       if (cut) {  // the last piece of a unit that other CTAs began
-        if (st & kLive) store_piece<D>(args, *sp, t, row, ocol, (st & kLater) != 0, valid, f, l);
+        if (st & kLive) store_piece<D>(args, 0, t, row, ocol, (st & kLater) != 0, valid, f, l);
       } else if ((st & kLater) && (st & kLive)) {
         const bool none = f == -INFINITY;  // the row sees no key
         const float inv_l = 1.f / l;
@@ -1089,6 +1090,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
+          __syncwarp();
           tmem_ld32(ocol + 32 * c, r);
           tmem_wait_ld();
           reg_fence32(r);
@@ -1159,7 +1161,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
             merge_with_own<D, BF16>(args, sg, t, row, ocol, active, valid, f, l);
           if (warp == 4) clear_flags(args, sg);
         } else {
-          if (st & kLive) store_piece<D>(args, sg, t, row, ocol, active, valid, f, l);
+          if (st & kLive) store_piece<D>(args, sg.own_slot, t, row, ocol, active, valid, f, l);
           mbar_arrive(bar(pbPiece + 1));
           if (warp == 4) {
             const bool all = early ? __all_sync(0xffffffffu, wait_bounded(bar(pbPiece + 1), 0, stop))
@@ -1187,7 +1189,6 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
     }
   }
-
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1214,8 +1215,7 @@ cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
   a.v_scale = static_cast<const uint8_t*>(L.v_scale);
   a.G = L.Hq / L.Hkv;
   a.tile_tok = kBM / a.G;
-  a.plan = PagedPlan{L.batch, DivBy(L.batch.page_size), L.Hkv, L.causal, 2 * a.tile_tok, L.opt[2],
-                     L.opt[0], L.opt[1]};
+  a.plan = PagedPlan{L.batch, DivBy(L.batch.page_size), L.Hkv, L.causal, 2 * a.tile_tok};
   a.box = L.box;
   a.box_bits = L.box_bits;
   a.scale_log2 = L.scale * kLog2e;

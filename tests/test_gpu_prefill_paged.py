@@ -192,6 +192,47 @@ def test_repeated_calls_are_bitwise_equal_with_a_stale_workspace(fa):
     assert fa.fa_get_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("D,kf,vf,heads", [
+    (64, "dense", "q4_0", (8, 8)), (64, "q4_0", "q4_0", (8, 2)), (64, "q4_0", "dense", (14, 2)),
+    (64, "dense", "dense", (3, 3)), (128, "q4_0", "dense", (8, 8)), (128, "q4_0", "q4_0", (28, 4)),
+    (128, "dense", "q4_0", (8, 2)), (128, "dense", "dense", (10, 2))])
+def test_units_cut_between_ctas(fa, D, kf, vf, heads):
+    """Prompts, chunks and single tokens whose units are cut into two to many pieces, merged by
+    whichever CTA comes last: every launch gives the same bytes."""
+    Hq, Hkv = heads
+    r = make_ragged([333, 1, 1021, 77, 600, 2], [333, 1500, 1400, 2100, 6000, 1030], Hkv, D, 64,
+                    "f16", kf, vf, seed=85)
+    q = make_q(sum(r.new), Hq, D, "f16", seed=86).cuda()
+    k, v, batch = r.pool(fa, "k"), r.pool(fa, "v"), r.batch()
+    first = fa.fa_prefill_paged(q, k, v, *batch)
+    check(r, q.cpu(), first.cpu())
+    o = torch.empty_like(first)
+    for _ in range(60):
+        o.fill_(7.0)
+        assert torch.equal(first, fa.fa_prefill_paged(q, k, v, *batch, o))
+    assert fa.fa_get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [(1, 1), (2, 1), (3, 1), (4, 2), (5, 1), (8, 1), (16, 1), (64, 1)])
+def test_one_token_over_many_pieces(fa, D, heads):
+    """Pieces of a few rows: the merge's threads share a row."""
+    Hq, Hkv = heads
+    for new, length, seed in (([1], [9000], 87), ([2], [3001], 88)):
+        r = make_ragged(new, length, Hkv, D, 64, "bf16", "dense", "q4_0", seed=seed)
+        q = make_q(new[0], Hq, D, "bf16", seed=seed + 10)
+        check(r, q, run(fa, r, q.cuda()).cpu())
+
+
+def test_more_sequences_than_a_warp(fa):
+    """The run is located 32 sequences at a time; empty ones among them."""
+    new = [(7 * i) % 5 for i in range(75)]
+    lens = [n + (311 * i) % 1700 for i, n in enumerate(new)]
+    r = make_ragged(new, lens, 2, 64, 64, "f16", "dense", "dense", seed=89)
+    q = make_q(sum(new), 8, 64, "f16", seed=90)
+    check(r, q, run(fa, r, q.cuda()).cpu())
+
+
 def test_captured_call_serves_other_batches(fa):
     """A captured call replayed after row_starts, seq_lens, the table and q were rewritten, and a
     second graph over the same workspace in between."""
