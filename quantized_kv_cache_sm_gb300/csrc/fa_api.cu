@@ -587,6 +587,8 @@ static fa_status paged_rows(bool append, const void* k_rows, const void* v_rows,
     return FA_ERR_INVALID_ARG;
   if (v_rows && !packed_ok(v_rows, rows, Hkv, D, v_row_stride, v_head_stride, !append))
     return FA_ERR_INVALID_ARG;
+  const int nsm = num_sms();
+  if (nsm < 1) return FA_ERR_CUDA;
   const int64_t pool_rows = static_cast<int64_t>(num_pages) * Hkv * page_size;
   const PagedBatch batch = {block_table, row_starts, seq_lens,  B,
                             rows,        num_pages,  page_size, pages_per_seq};
@@ -596,7 +598,7 @@ static fa_status paged_rows(bool append, const void* k_rows, const void* v_rows,
                  D),
       paged_side(v_rows, v_row_stride, v_head_stride, v_pages, v_format == FA_KV_Q4_0, pool_rows,
                  D),
-      Hkv, D, dtype == FA_BF16, reinterpret_cast<cudaStream_t>(stream));
+      Hkv, D, dtype == FA_BF16, nsm, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

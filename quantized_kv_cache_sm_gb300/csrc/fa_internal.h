@@ -125,7 +125,7 @@ struct PagedSide {
   bool q4;
 };
 cudaError_t paged_rows_launch(bool append, const PagedBatch& b, const PagedSide& k,
-                              const PagedSide& v, int Hkv, int D, bool bf16,
+                              const PagedSide& v, int Hkv, int D, bool bf16, int num_sms,
                               cudaStream_t stream);
 uint32_t paged_take_error();
 

@@ -260,3 +260,51 @@ def test_read_is_exact_at_the_values_bounds(fa):
         for t, x in expected_read(r, "k", 8).items():
             assert torch.equal(out[t].cpu(), x), (dtype, t)
         assert np.isfinite(np64(out)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_every_value_quantizes_as_in_the_contiguous_call(fa, dtype):
+    """All 2^16 bit patterns (infinities and NaN among them), in order and shuffled, and blocks of few
+    distinct magnitudes, whose largest recurs in any lane with either sign: the bits that the
+    contiguous quantizer stores."""
+    D, page = 128, 64
+    g = torch.Generator().manual_seed(11)
+    every = torch.arange(65536, dtype=torch.int32)
+    few = torch.tensor([-3.0, -1.5, 0.0, 1.5, 3.0]).to(DT[dtype])
+    x = torch.cat([every.to(torch.int16), every[torch.randperm(65536, generator=g)].to(torch.int16),
+                   few[torch.randint(5, (65536,), generator=g)].view(torch.int16)])
+    x = x.view(DT[dtype]).reshape(-1, 1, D).cuda()
+    rows = x.shape[0]
+    assert rows % page == 0
+    want = fa.fa_quantize_q4_0(x.reshape(1, 1, rows, D))
+    pools = [fa.Q4Tensor(torch.zeros_like(want.buf), rows // page, 1, page, D) for _ in "kv"]
+    table = torch.arange(rows // page, dtype=torch.int32, device="cuda")[None]
+    starts = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([rows], dtype=torch.int32, device="cuda")
+    fa.fa_append_paged(x, x, *pools, table, starts, lens)
+    assert fa.fa_get_status() == fa.FA_OK
+    n = rows * D // 2
+    for p in pools:
+        assert torch.equal(p.buf[:n], want.buf[:n])
+        assert torch.equal(p.buf[-rows * D // 16:], want.buf[-rows * D // 16:])
+
+
+@pytest.mark.parametrize("Hkv,D,rows", [(1, 128, 5003), (1, 64, 9001), (5, 64, 700), (5, 128, 3001),
+                                        (3, 160, 1777), (40, 32, 333), (7, 256, 211), (64, 128, 5)])
+def test_rows_and_heads_split_over_ctas(fa, Hkv, D, rows):
+    """Several groups of rows per CTA, part of the heads per CTA, the last of each short."""
+    new, lens = [rows - 2 * (rows // 3), 0, 2 * (rows // 3)], [rows, 3, rows]
+    r = make_ragged(new, lens, Hkv, D, 32, "f16", "q4_0", "dense", seed=rows)
+    k_out = torch.empty(rows, Hkv, D, dtype=torch.float16, device="cuda")
+    v_out = torch.empty_like(k_out)
+    fa.fa_read_paged(r.pool(fa, "k"), r.pool(fa, "v"), *r.batch(), k_out, v_out)
+    for side, out in (("k", k_out), ("v", v_out)):
+        want = expected_read(r, side, rows)
+        assert torch.equal(bits(out.cpu()), bits(torch.stack([want[t] for t in range(rows)])))
+    g = torch.Generator().manual_seed(12)
+    k_new, v_new = (torch.randn(rows, Hkv, D, generator=g).half() for _ in "kv")
+    k, v = r.pool(fa, "k"), r.pool(fa, "v")
+    fa.fa_append_paged(k_new.cuda(), v_new.cuda(), k, v, *r.batch())
+    assert fa.fa_get_status() == fa.FA_OK
+    assert torch.equal(stored(k), bits(after_append(r, "k", k_new)))
+    assert torch.equal(stored(v), bits(after_append(r, "v", v_new)))
