@@ -51,6 +51,8 @@ def library_path() -> str:
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the CUDA library once per process (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             _lib = load_from(path or _build.LIB_PATH)
@@ -192,7 +194,7 @@ def _check_q4(t: Q4Tensor, what: str):
     """A Q4Tensor's buffer must be one contiguous uint8 vector holding both planes."""
     if t.buf.dtype != torch.uint8 or t.buf.dim() != 1 or not t.buf.is_contiguous():
         raise ValueError(f"{what}: the q4_0 buffer must be a contiguous uint8 vector")
-    need = fa_q4_0_bytes(t.B, t.H, t.S, t.D)
+    need = _q4_0_bytes(t.B, t.H, t.S, t.D)
     if need == 0 or t.buf.numel() < need:
         raise ValueError(f"{what}: a q4_0 tensor of shape {t.shape} needs {need} bytes, "
                          f"its buffer holds {t.buf.numel()}")
@@ -294,12 +296,12 @@ def fa_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, q_pos_offset, causal) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _q4_0_bytes(B: int, H: int, S: int, D: int) -> int:
-    return int(load().fa_q4_0_bytes(B, H, S, D))
+    return int(load().fa_q4_0_bytes(int(B), int(H), int(S), int(D)))
 
 
 def fa_q4_0_bytes(B, H, S, D) -> int:
     # a pure function of the shape, asked on every call that takes a q4_0 tensor: cached
-    return _q4_0_bytes(int(B), int(H), int(S), int(D))
+    return _q4_0_bytes(B, H, S, D)
 
 
 def fa_q4_0_scale_offset(B, H, S, D) -> int:
@@ -607,28 +609,30 @@ def fa_decode_paged(q, k_pages, v_pages, block_table: torch.Tensor, seq_lens: to
     return o
 
 
-# The paged calls check their arguments with few calls into torch: a decode step's append takes 3 us
-# on the GPU, and each look at a tensor 0.1 to 0.3 us here.
+# The paged calls are checked with few looks at their tensors, each 0.05 to 0.15 us: a decode step's
+# append takes 3 us on the GPU.
 
 def _paged_batch(block_table, row_starts, seq_lens):
     """(B, pages_per_seq) of a ragged batch's device arrays (see fa.h, packed rows)."""
-    shapes = block_table.shape, row_starts.shape, seq_lens.shape
-    for name, t, shape, dim in (("block_table", block_table, shapes[0], 2),
-                                ("row_starts", row_starts, shapes[1], 1),
-                                ("seq_lens", seq_lens, shapes[2], 1)):
-        if t.dtype != torch.int32 or len(shape) != dim or not t.is_contiguous():
+    i32 = torch.int32
+    table = block_table.shape
+    if (block_table.dtype is i32 and row_starts.dtype is i32 and seq_lens.dtype is i32
+            and len(table) == 2 and row_starts.shape == (table[0] + 1,)
+            and seq_lens.shape == (table[0],) and block_table.is_contiguous()
+            and row_starts.is_contiguous() and seq_lens.is_contiguous()):
+        return table
+    for name, t, dim in (("block_table", block_table, 2), ("row_starts", row_starts, 1),
+                         ("seq_lens", seq_lens, 1)):
+        if t.dtype != i32 or t.dim() != dim or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
-    B, pps = shapes[0]
-    if shapes[2][0] != B or shapes[1][0] != B + 1:
-        raise ValueError("block_table [B, pages_per_seq], row_starts [B + 1] and seq_lens [B] must "
-                         "describe the same B sequences")
-    return B, pps
+    raise ValueError("block_table [B, pages_per_seq], row_starts [B + 1] and seq_lens [B] must "
+                     "describe the same B sequences")
 
 
 def _packed(t, what, dtype, heads, D, rows):
     """(pointer, row stride, head stride) of packed rows [rows, heads, D] with contiguous
     innermost; strides of dimensions of one entry are not used and passed as D."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if t.shape != (rows, heads, D):
         raise ValueError(f"{what} must be a [{rows}, {heads}, {D}] tensor")
@@ -638,19 +642,25 @@ def _packed(t, what, dtype, heads, D, rows):
     return t.data_ptr(), row if rows > 1 else D, head if heads > 1 else D
 
 
-def _paged_pools(k_pages, v_pages, dtype):
-    kf, shape = _side(k_pages)
-    if kf == FA_KV_DENSE and k_pages.dtype != dtype:
+def _paged_pool(t, dtype):
+    """(format code, [num_pages, Hkv, page_size, D], the tensor that holds it) of one pool."""
+    fmt, shape = _side(t)
+    if fmt == FA_KV_Q4_0:
+        return fmt, shape, t.buf
+    if t.dtype is not dtype:
         raise TypeError(f"dense pools must be {dtype}, as the packed rows are")
-    vf = kf
-    if v_pages is not None:
-        vf, vshape = _side(v_pages)
-        if vshape != shape:
-            raise ValueError("k_pages and v_pages must have the same [num_pages, Hkv, page_size, "
-                             "D]")
-        if vf == FA_KV_DENSE and v_pages.dtype != dtype:
-            raise TypeError(f"dense pools must be {dtype}, as the packed rows are")
-    return kf, vf, shape
+    return fmt, shape, t
+
+
+def _paged_pools(k_pages, v_pages, dtype):
+    """Both formats, the shape that both pools have, and the tensors that hold them."""
+    kf, shape, kt = _paged_pool(k_pages, dtype)
+    if v_pages is None:
+        return kf, kf, shape, kt, None
+    vf, vshape, vt = _paged_pool(v_pages, dtype)
+    if vshape != shape:
+        raise ValueError("k_pages and v_pages must have the same [num_pages, Hkv, page_size, D]")
+    return kf, vf, shape, kt, vt
 
 
 def _launch_stream(stream, device: int) -> int:
@@ -659,7 +669,7 @@ def _launch_stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
-def _paged_rows(fn, k, v, k_pages, v_pages, block_table, row_starts, seq_lens, stream):
+def _paged_rows(append, k, v, k_pages, v_pages, block_table, row_starts, seq_lens, stream):
     """The arguments that fa_append_paged and fa_read_paged share, checked and passed on."""
     if (v is None) != (v_pages is None):
         raise ValueError("give both V rows and v_pages, or neither")
@@ -667,16 +677,21 @@ def _paged_rows(fn, k, v, k_pages, v_pages, block_table, row_starts, seq_lens, s
         raise ValueError("packed rows must be [rows, Hkv, D]")
     rows, dtype = k.shape[0], k.dtype
     dt = _dtype_code(dtype)
-    kf, vf, (NP, Hkv, page, D) = _paged_pools(k_pages, v_pages, dtype)
+    kf, vf, (NP, Hkv, page, D), kt, vt = _paged_pools(k_pages, v_pages, dtype)
     B, pps = _paged_batch(block_table, row_starts, seq_lens)
     kp, krs, khs = _packed(k, "K rows", dtype, Hkv, D, rows)
-    vp, vrs, vhs = (None, D, D) if v is None else _packed(v, "V rows", dtype, Hkv, D, rows)
-    device = _on_device(k, v, k_pages, v_pages, block_table, row_starts, seq_lens)
-    pk, pv = k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr()
-    ptrs = (kp, vp, pk, pv) if fn == "fa_append_paged" else (pk, pv, kp, vp)
-    _check(getattr(load(), fn)(*ptrs, block_table.data_ptr(), row_starts.data_ptr(),
-                               seq_lens.data_ptr(), B, rows, Hkv, D, NP, page, pps, krs, khs, vrs,
-                               vhs, dt, kf, vf, _launch_stream(stream, device)), fn)
+    pk, pv, vp, vrs, vhs = kt.data_ptr(), None, None, D, D
+    if v is not None:
+        vp, vrs, vhs = _packed(v, "V rows", dtype, Hkv, D, rows)
+        pv = vt.data_ptr()
+    device = _on_device(k, v, kt, vt, block_table, row_starts, seq_lens)
+    shared = (block_table.data_ptr(), row_starts.data_ptr(), seq_lens.data_ptr(), B, rows, Hkv, D,
+              NP, page, pps, krs, khs, vrs, vhs, dt, kf, vf, _launch_stream(stream, device))
+    lib = load()
+    if append:
+        _check(lib.fa_append_paged(kp, vp, pk, pv, *shared), "fa_append_paged")
+    else:
+        _check(lib.fa_read_paged(pk, pv, kp, vp, *shared), "fa_read_paged")
 
 
 def fa_append_paged(k_new: torch.Tensor, v_new: torch.Tensor | None, k_pages, v_pages,
@@ -687,7 +702,7 @@ def fa_append_paged(k_new: torch.Tensor, v_new: torch.Tensor | None, k_pages, v_
     Hkv, page_size, D], each dense or a Q4Tensor; block_table [B, pages_per_seq], row_starts [B + 1]
     and seq_lens [B] (lengths with the new tokens) int32 on the device.  v_new and v_pages may both
     be None."""
-    _paged_rows("fa_append_paged", k_new, v_new, k_pages, v_pages, block_table, row_starts,
+    _paged_rows(True, k_new, v_new, k_pages, v_pages, block_table, row_starts,
                 seq_lens, stream)
 
 
@@ -697,7 +712,7 @@ def fa_read_paged(k_pages, v_pages, block_table: torch.Tensor, row_starts: torch
     """The inverse of fa_append_paged: the last row_starts[b + 1] - row_starts[b] tokens of every
     sequence, read out of the pages into packed rows k_out, v_out [rows, Hkv, D] (q4_0 pools
     dequantized).  Returns (k_out, v_out)."""
-    _paged_rows("fa_read_paged", k_out, v_out, k_pages, v_pages, block_table, row_starts, seq_lens,
+    _paged_rows(False, k_out, v_out, k_pages, v_pages, block_table, row_starts, seq_lens,
                 stream)
     return k_out, v_out
 
@@ -722,7 +737,7 @@ def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tenso
     rows, Hq, D = q.shape
     dtype = q.dtype
     dt = _dtype_code(dtype)
-    kf, vf, (NP, Hkv, page, Dk) = _paged_pools(k_pages, v_pages, dtype)
+    kf, vf, (NP, Hkv, page, Dk), kt, vt = _paged_pools(k_pages, v_pages, dtype)
     if Dk != D:
         raise ValueError("head dim of the pools does not match q")
     B, pps = _paged_batch(block_table, row_starts, seq_lens)
@@ -731,7 +746,7 @@ def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tenso
             o = torch.zeros((rows, Hq, D), dtype=dtype, device=q.device)
     qp, qrs, qhs = _packed(q, "q", dtype, Hq, D, rows)
     op, ors, ohs = _packed(o, "o", dtype, Hq, D, rows)
-    device = _on_device(q, k_pages, v_pages, o, block_table, row_starts, seq_lens, workspace)
+    device = _on_device(q, kt, vt, o, block_table, row_starts, seq_lens, workspace)
     lib = load()
     if workspace is None:
         need = max(lib.fa_prefill_paged_workspace_bytes(Hq, Hkv, D), 16)
@@ -742,7 +757,7 @@ def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tenso
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     if scale is None:
         scale = D ** -0.5
-    _check(lib.fa_prefill_paged(qp, k_pages.data_ptr(), v_pages.data_ptr(), op,
+    _check(lib.fa_prefill_paged(qp, kt.data_ptr(), vt.data_ptr(), op,
                                 block_table.data_ptr(), row_starts.data_ptr(), seq_lens.data_ptr(),
                                 B, rows, Hq, Hkv, D, NP, page, pps, qrs, qhs, ors, ohs,
                                 int(bool(causal)), float(scale), dt, kf, vf, workspace.data_ptr(),
