@@ -133,6 +133,34 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
     }
   }
 }
+// Dq<true> with (n - 8) d formed in bf16 pairs: d = hi + lo, each exact in bf16 (an f16 scale's 11
+// bits), (n - 8) lo is exact (4 and 3 bits), and the fused (n - 8) hi + (n - 8) lo rounds the exact
+// sum once, as the product in f32 does, in four instructions a pair for seven.  (One token each
+// against 64 sequences of 8192 q4_0 keys, 8 kv heads, D = 128: 377 -> 339 us.)
+struct DqSplit : Dq<true> {
+  struct Scale {
+    __nv_bfloat162 hi, lo;
+  };
+  static __device__ __forceinline__ Scale block(__half d) {
+    const float f = __half2float(d);
+    const __nv_bfloat16 hi = __float2bfloat16_rn(f);
+    const float lo = f - __bfloat162float(hi);
+    // (an infinite d has no low part)
+    return {__bfloat162bfloat162(hi), __float2bfloat162_rn(lo == lo ? lo : 0.f)};
+  }
+  static __device__ __forceinline__ uint32_t scale(__nv_bfloat162 v, Scale d) {
+    const __nv_bfloat162 r = __hfma2(v, d.hi, __hmul2(v, d.lo));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+template <bool BF16>
+struct DqOf {
+  using type = Dq<false>;
+};
+template <>
+struct DqOf<true> {
+  using type = DqSplit;
+};
 // 16-byte asynchronous copy of which src_bytes are read, the rest zeros
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -956,8 +984,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           for (int k = 0; k < (kItems + C::kDqThreads - 1) / C::kDqThreads; ++k) {
             const int it = u + k * C::kDqThreads;
             if (kItems % C::kDqThreads == 0 || it < kItems)
-              dequant_item<D, BF16, C::kNibRow, C::kScaleRow, C::kRawNib>(raw, dst, it % kBN,
-                                                                          it / kBN, mg);
+              dequant_item<D, BF16, C::kNibRow, C::kScaleRow, C::kRawNib,
+                           typename DqOf<BF16>::type>(raw, dst, it % kBN, it / kBN, mg);
           }
           // generic-proxy writes must be visible to the tensor core's async proxy
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

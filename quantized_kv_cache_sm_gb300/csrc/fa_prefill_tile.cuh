@@ -90,6 +90,7 @@ struct Dq<false> {
     const __half2 c = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));  // -72
     return __hfma2(*reinterpret_cast<__half2*>(&x), s, c);
   }
+  static __device__ __forceinline__ __half block(__half d) { return d; }
   static __device__ __forceinline__ uint32_t scale(__half2 v, __half d) {
     __half2 r = __hmul2(v, __halves2half2(d, d));
     return *reinterpret_cast<uint32_t*>(&r);
@@ -108,6 +109,7 @@ struct Dq<true> {
   static __device__ __forceinline__ __nv_bfloat162 hi(uint32_t w, uint32_t mg) {
     return lo(w >> 4, mg);
   }
+  static __device__ __forceinline__ float block(__half d) { return __half2float(d); }
   static __device__ __forceinline__ uint32_t scale(__nv_bfloat162 v, float d) {
     // (n - 8) * d rounded once to bf16: the product of a 4-bit integer and an fp16 value is
     // exact in f32, so round only after the f32 multiply.
@@ -273,7 +275,7 @@ __device__ __forceinline__ void softmax_block(uint32_t scol, uint32_t ocol, bool
 // One q4_0 dequant item: the 32 elements of block blk of key row t of a raw tile (nibble rows of
 // NIB bytes, 64B-swizzled at D = 128 and 32B-swizzled at D = 64, then the fp16 scale rows of SROW
 // bytes from byte RAWNIB), expanded to (q - 8) * d in f16/bf16 into the 128B-swizzled ring stage.
-template <int D, bool BF16, int NIB, int SROW, int RAWNIB>
+template <int D, bool BF16, int NIB, int SROW, int RAWNIB, class Q = Dq<BF16>>
 __device__ __forceinline__ void dequant_item(const uint8_t* raw, uint8_t* dst, int t, int blk,
                                              uint32_t mg) {
   const uint8_t* nrow = raw + t * NIB;
@@ -289,18 +291,11 @@ __device__ __forceinline__ void dequant_item(const uint8_t* raw, uint8_t* dst, i
       // bytes 4q..4q+3 -> elements 4q..4q+3 (low) and 4q+16..4q+19 (high)
       const uint32_t a = __byte_perm(w[q], 0u, 0x5150);   // byte0 at b0, byte1 at b2
       const uint32_t c2 = __byte_perm(w[q], 0u, 0x5352);  // byte2 at b0, byte3 at b2
-      if (BF16) {
-        const float d = __half2float(dh);
-        outv[2 * q + 0] = Dq<true>::scale(Dq<true>::lo(a, mg), d);
-        outv[2 * q + 1] = Dq<true>::scale(Dq<true>::lo(c2, mg), d);
-        outv[8 + 2 * q + 0] = Dq<true>::scale(Dq<true>::hi(a, mg), d);
-        outv[8 + 2 * q + 1] = Dq<true>::scale(Dq<true>::hi(c2, mg), d);
-      } else {
-        outv[2 * q + 0] = Dq<false>::scale(Dq<false>::lo(a, mg), dh);
-        outv[2 * q + 1] = Dq<false>::scale(Dq<false>::lo(c2, mg), dh);
-        outv[8 + 2 * q + 0] = Dq<false>::scale(Dq<false>::hi(a, mg), dh);
-        outv[8 + 2 * q + 1] = Dq<false>::scale(Dq<false>::hi(c2, mg), dh);
-      }
+      const auto d = Q::block(dh);
+      outv[2 * q + 0] = Q::scale(Q::lo(a, mg), d);
+      outv[2 * q + 1] = Q::scale(Q::lo(c2, mg), d);
+      outv[8 + 2 * q + 0] = Q::scale(Q::hi(a, mg), d);
+      outv[8 + 2 * q + 1] = Q::scale(Q::hi(c2, mg), d);
     }
     // elements 32 blk + 8 cc .. +7 form 16-byte chunk (4 blk + cc) of the row
 #pragma unroll

@@ -8,7 +8,7 @@ import torch
 
 import oracle
 from gpu_common import check_close, np64
-from paged_common import DT, make_ragged
+from paged_common import DT, make_ragged, q4_buffer, q4_planes
 
 pytestmark = pytest.mark.gpu
 
@@ -327,3 +327,34 @@ def test_no_rows(fa):
     assert o.shape == (0, 8, 128)
     o = run(fa, r, make_q(3, 8, 128, "f16", seed=123))  # padding only
     assert (o == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_scale_is_dequantized_as_read(fa, dtype, D):
+    """One key a sequence has weight 1 whatever its (here zero) score: o is the value row itself, for
+    every finite scale and all codes what fa_read_paged gives, products past the type's range
+    included."""
+    Hkv, page = 8, 16
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    scales = every[torch.isfinite(every.view(torch.float16))]
+    blocks = Hkv * D // 32
+    B = -(-scales.numel() // blocks)
+    g = torch.Generator().manual_seed(131)
+    buf = torch.zeros(fa.fa_q4_0_bytes(B, Hkv, page, D), dtype=torch.uint8)
+    nib, sc = q4_planes(buf, (B, Hkv, page, D))
+    nib.copy_(torch.randint(256, nib.shape, generator=g, dtype=torch.uint8))
+    sc[:, :, 0] = scales.repeat(2)[:B * blocks].view(B, Hkv, D // 32)
+    pool = fa.Q4Tensor(buf.cuda(), B, Hkv, page, D)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    q = make_q(B, Hkv, D, dtype, seed=132).cuda()
+    zeros = torch.zeros(B, Hkv, page, D, dtype=DT[dtype])
+    keys = fa.Q4Tensor(q4_buffer(zeros).cuda(), B, Hkv, page, D)
+    want = torch.empty_like(q)
+    fa.fa_read_paged(pool, None, table, starts, lens, want)
+    assert fa.fa_get_status() == fa.FA_OK
+    for k in (keys, zeros.cuda()):
+        assert torch.equal(fa.fa_prefill_paged(q, k, pool, table, starts, lens), want)
+    assert fa.fa_get_status() == fa.FA_OK
