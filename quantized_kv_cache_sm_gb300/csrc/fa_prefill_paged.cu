@@ -29,6 +29,7 @@
 // Warp roles: as in fa_prefill.cu (0 producer and scheduler, 1 TMEM and MMA issuer, 2-3 and 12-15
 // q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B).
 #include <limits.h>
+#include <stddef.h>
 
 #include "fa_internal.h"
 #include "fa_paged.cuh"
@@ -75,7 +76,7 @@ constexpr int kOffPlan = kOffMerge + 16;  // int: the run has segments; raw tile
 constexpr int kOffSegQ = 512;            // the segment queue
 
 // one segment: steps [j0, j1) of a unit
-struct PSeg {
+struct alignas(16) PSeg {
   int row0;       // packed row of tile A's first token
   int g;          // kv head
   int tokA, tokB; // tokens of the tiles (0: tile absent)
@@ -86,7 +87,10 @@ struct PSeg {
   int c_first, c_last;  // CTAs of the unit's first and last step (equal: not cut)
   int slot_first;       // partial slot of the first one's piece (the others' is 0)
   int own_slot;         // and of this CTA's
+  int unused[2];
 };
+static_assert(offsetof(PSeg, pos0) == 16 && offsetof(PSeg, j0) == 32 &&
+                  offsetof(PSeg, slot_first) == 48 && sizeof(PSeg) == 64, "read_seg");
 constexpr int kOffFirst = kOffSegQ + kSegQ * 64;  // the first segment, kept for its merge
 static_assert(sizeof(PSeg) <= 64 && kOffFirst + 64 <= 512 + 1024, "segment queue");
 static_assert(kOffPlan + 8 <= kOffSegQ, "barrier area");
@@ -107,10 +111,11 @@ struct PArgs {
 // One tile of a piece, column-major, so that a warp's 32 rows of one column are 128 contiguous
 // bytes: [D + 2 columns][128 rows] f32, columns O[0..D), frame, row sum.  (Row-major pieces, stored
 // 16 bytes a lane and row, took the 2048-token chunk at 16384 keys from 346 to 368 us.)  A CTA has
-// two slots: 0 for the piece its run begins with, 1 for one that it reaches after other units.
+// two slots: 0 for the piece its run begins with, 1 for one that it reaches after other units (an
+// address stays within them whatever the slot).
 template <int D>
 __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t) {
-  return part + ((static_cast<int64_t>(c) * 2 + slot) * 2 + t) * (D + 2) * kBM;
+  return part + ((static_cast<int64_t>(c) * 2 + (slot & 1)) * 2 + t) * (D + 2) * kBM;
 }
 
 // the thread's number, formed anew where it is asked for
@@ -161,6 +166,23 @@ template <>
 struct DqOf<true> {
   using type = DqSplit;
 };
+// A segment out of shared memory, whole and unconditionally.  (Fields read one by one where they were
+// needed left it to the compiler to read some of them under a condition, and in the layout with q4_0
+// sides such a selection, `own CTA first ? slot_first : 0`, now and then gave 512 for 0 to a whole
+// warp, whose rows then went outside the workspace.  No build that reads them unconditionally did.)
+__device__ __forceinline__ int4 lds_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ PSeg read_seg(uint32_t addr) {
+  const int4 a = lds_int4(addr), b = lds_int4(addr + 16), c = lds_int4(addr + 32),
+             d = lds_int4(addr + 48);
+  return PSeg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w, d.x, d.y, {0, 0}};
+}
 // 16-byte asynchronous copy of which src_bytes are read, the rest zeros
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -244,86 +266,73 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
   }
 }
 
-// The same for at most kFewPieces pieces and a thread's own row, whose own piece is still in tensor
-// memory, 32 columns at a time.  The pieces are joined in CTA order with the arithmetic of
+// The same for a thread's own row of a unit of two pieces, the own one still in tensor memory: 64
+// columns of the other one's in flight.  The pieces are joined in CTA order with the arithmetic of
 // merge_pieces, so that the result does not depend on which CTA came last.
-constexpr int kFewPieces = 3;
 template <int D, bool BF16>
 __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg, int t, int row,
                                                uint32_t ocol, bool active, bool valid, float f,
                                                float l) {
-  const int64_t step = 4 * (D + 2) * kBM;  // floats from a CTA's slot 0 to the next CTA's
-  const float* p_first = piece_tile<D>(args.part, sg.c_first, sg.slot_first, t) + row;
-  const float* p_rest = piece_tile<D>(args.part, sg.c_first, 0, t) + row;
-  const int n = sg.c_last - sg.c_first + 1, own = static_cast<int>(blockIdx.x) - sg.c_first;
-  float w[kFewPieces], lc[kFewPieces];
+  const bool own_first = sg.c_first == static_cast<int>(blockIdx.x);
+  const float* p = piece_tile<D>(args.part, own_first ? sg.c_last : sg.c_first,
+                                 own_first ? 0 : sg.slot_first, t) + row;
+  float v[2][32];
+  auto load = [&](float(&to)[32], int k) {
+    if (valid && k < D) {
 #pragma unroll
-  for (int c = 0; c < kFewPieces; ++c) {
-    const bool in = valid && c < n && c != own;
-    const float* p = c == 0 ? p_first : p_rest + c * step;
-    w[c] = in ? __ldcg(p + D * kBM) : -INFINITY;
-    lc[c] = in ? __ldcg(p + (D + 1) * kBM) : 0.f;
-    if (c == own && active) {
-      w[c] = f;
-      lc[c] = l;
+      for (int i = 0; i < 32; ++i) to[i] = __ldcg(p + (k + i) * kBM);
     }
-  }
-  const float F = fmaxf(w[0], fmaxf(w[1], w[2]));
+  };
+  const float fo = valid ? __ldcg(p + D * kBM) : -INFINITY;
+  const float lo = valid ? __ldcg(p + (D + 1) * kBM) : 0.f;
+  load(v[0], 0);
+  load(v[1], 32);
+  if (!active) f = -INFINITY;
+  const float F = fmaxf(f, fo);
+  const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O is not a number
+  const float wo = fo == -INFINITY ? 0.f : ex2(fo - F);
   float L = 0.f;
 #pragma unroll
-  for (int c = 0; c < kFewPieces; ++c) {
-    w[c] = w[c] == -INFINITY ? 0.f : ex2(w[c] - F);  // 0: the piece's O is not a number
-    if (w[c] != 0.f) L = fmaf(w[c], lc[c], L);
+  for (int c = 0; c < 2; ++c) {
+    const bool mine = (c == 0) == own_first;
+    if ((mine ? w : wo) != 0.f) L = fmaf(mine ? w : wo, mine ? l : lo, L);
   }
   const float inv = F == -INFINITY ? 0.f : 1.f / L;
   const int tok = row / args.G;
   uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
                   (sg.g * args.G + (row - tok * args.G)) * args.o_head_stride;
 #pragma unroll 1
-  for (int k = 0; k < D; k += 32) {
-    uint32_t r[32];
-    __syncwarp();  // the loads from tensor memory are the whole warp's
-    if (active) {
-      tmem_ld32(ocol + k, r);
-      tmem_wait_ld();
-      reg_fence32(r);
-    }
-    if (!valid) continue;
-    float v[kFewPieces - 1][32];  // the other pieces' columns, all loads in flight together
+  for (int k0 = 0; k0 < D; k0 += 64) {
 #pragma unroll
-    for (int x = 0; x < kFewPieces - 1; ++x) {
-      const int c = x < own ? x : x + 1;
-      const float* p = (c == 0 ? p_first : p_rest + c * step) + k * kBM;
-      if (c < n) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[x][i] = __ldcg(p + i * kBM);
+    for (int half = 0; half < 2; ++half) {
+      const int k = k0 + 32 * half;
+      uint32_t r[32];
+      __syncwarp();  // the loads from tensor memory are the whole warp's
+      if (active) {
+        tmem_ld32(ocol + k, r);
+        tmem_wait_ld();
+        reg_fence32(r);
       }
-    }
-    float acc[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < kFewPieces; ++c) {
-      if (w[c] == 0.f) continue;
+      float acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float x = c == own                                ? __uint_as_float(r[i])
-                        : c == 0 || (c == 1 && own == 0)        ? v[0][i]
-                                                                : v[1][i];
-        acc[i] = fmaf(w[c], x, acc[i]);
+        const float a = w != 0.f ? __uint_as_float(r[i]) : 0.f;
+        const float b = wo != 0.f ? v[half][i] : 0.f;
+        acc[i] = own_first ? fmaf(wo, b, fmaf(w, a, 0.f)) : fmaf(w, a, fmaf(wo, b, 0.f));
+      }
+      load(v[half], k + 64);
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (valid) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4*>(orow + 2 * k)[i] =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       }
     }
-    uint32_t pk[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(orow + 2 * k)[i] =
-          make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
   }
 }
-
-// Publication flag of CTA c's piece
 __device__ __forceinline__ uint32_t* piece_flag(const PArgs& args, const PSeg& sg, int c) {
   return args.pflags + 2 * c + (c == sg.c_first ? sg.slot_first : 0);
 }
@@ -338,9 +347,7 @@ __device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, 
   return all;
 }
 
-// Store of a thread's row of a piece into one of the CTA's slots.  (The slot is passed in, not
-// selected here by `cta == sg.c_first ? sg.slot_first : 0`: in the build whose softmax warps take
-// registers over, that conditional load gave now and then 512 for 0, a warp at a time.)
+// Store of a thread's row of a piece into one of the CTA's slots
 template <int D>
 __device__ __forceinline__ void store_piece(const PArgs& args, int slot, int t, int row,
                                             uint32_t ocol, bool active, bool valid, float f,
@@ -407,6 +414,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bgen + kOffTmem);
   volatile int* has_run = reinterpret_cast<volatile int*>(bgen + kOffPlan);
   volatile int* raw_end = has_run + 1;
+  const uint32_t segs = bar0 + kOffSegQ;
   auto seg_at = [&](int i) -> PSeg* {
     return reinterpret_cast<PSeg*>(bgen + kOffSegQ + (i % kSegQ) * 64);
   };
@@ -817,11 +825,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           ok = mbar_wait(bar(pbSegFull + sidx % kSegQ), (sidx / kSegQ) & 1, abort_flag,
                          &g_prefill_paged_error);
           if (!ok) break;
-          const PSeg* sp = seg_at(sidx);
-          const int j0 = sp->j0, j1 = sp->j1;
+          const PSeg sg = read_seg(segs + (sidx % kSegQ) * 64);
+          const int j0 = sg.j0, j1 = sg.j1;
           if (j1 < 0) break;
-          const int eA = min(j1, sp->nbA), eB = min(j1, sp->nbB);
-          const bool sp_lone = sp->tokB == 0;
+          const int eA = min(j1, sg.nbA), eB = min(j1, sg.nbB);
+          const bool sp_lone = sg.tokB == 0;
           mbar_arrive(bar(pbSegEmpty + sidx % kSegQ));
           ok = mbar_wait(bar(pbQFull), sidx & 1, abort_flag, &g_prefill_paged_error);
           tc_fence_after();
@@ -1035,18 +1043,18 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       f = -INFINITY;
       l = 0.f;
       {
-        const PSeg* sp = seg_at(sidx);
-        const int j0 = sp->j0, j1 = sp->j1;
+        const PSeg sg = read_seg(segs + (sidx % kSegQ) * 64);
+        const int j0 = sg.j0, j1 = sg.j1;
         if (j1 < 0) break;
         const int tid = opaque_tid();
         const int t = tid >= 256 ? 1 : 0, row = tid & 127;
-        const int ntok = t ? sp->tokB : sp->tokA;
-        left = ntok > 0 ? max(0, min(j1, t ? sp->nbB : sp->nbA) - j0) : 0;
-        const int last = sp->len - 1;
-        rel = (plan.causal ? min(last, sp->pos0 + t * args.tile_tok + row / args.G) : last) -
+        const int ntok = t ? sg.tokB : sg.tokA;
+        left = ntok > 0 ? max(0, min(j1, t ? sg.nbB : sg.nbA) - j0) : 0;
+        const int last = sg.len - 1;
+        rel = (plan.causal ? min(last, sg.pos0 + t * args.tile_tok + row / args.G) : last) -
               j0 * kBN;
         st = (st & (kPhS | kPhAlt | kPhPv | kPhO | kFirstCut)) | (t ? kTileB : 0) |
-             ((row & ~31) < ntok * args.G ? kLive : 0) | (kAlt && sp->tokB == 0 ? kLone : 0);
+             ((row & ~31) < ntok * args.G ? kLive : 0) | (kAlt && sg.tokB == 0 ? kLone : 0);
         tm = *reinterpret_cast<volatile uint32_t*>(tmem_slot) +
              (static_cast<uint32_t>(row & ~31) << 16);
       }
@@ -1088,19 +1096,19 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
       if (!ok) break;
       open = true;
-      const PSeg* sp = seg_at(sidx);
+      const PSeg sg = read_seg(segs + (sidx % kSegQ) * 64);
       const int tid = opaque_tid();
       const int t = tid >= 256 ? 1 : 0, row = tid & 127;  // query tile, this thread's row
       const int rtok = row / args.G;                      // the row's token within the tile
-      const int ntok = t ? sp->tokB : sp->tokA;
+      const int ntok = t ? sg.tokB : sg.tokA;
       const uint32_t ocol = tm + (t ? C::kColO1 : C::kColO0);
       if constexpr (C::kPaired) {
-        const int j0 = sp->j0, j1 = sp->j1;
-        const int n = ntok > 0 ? max(0, min(j1, t ? sp->nbB : sp->nbA) - j0) : 0;
+        const int j0 = sg.j0, j1 = sg.j1;
+        const int n = ntok > 0 ? max(0, min(j1, t ? sg.nbB : sg.nbA) - j0) : 0;
         ks = (ks + j1 - j0 - n + 1) % C::kSlots;
       }
-      if (sp->c_last != cta) break;  // the run ends inside the unit: below
-      const bool cut = sp->c_first != cta;
+      if (sg.c_last != cta) break;  // the run ends inside the unit: below
+      const bool cut = sg.c_first != cta;
       if (st & kLater) {  // the tile had key blocks in this segment
         ok = wait_bounded(bar(pbODone + t), (st >> 3) & 1, stop);
         st ^= kPhO;
@@ -1113,8 +1121,8 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       } else if ((st & kLater) && (st & kLive)) {
         const bool none = f == -INFINITY;  // the row sees no key
         const float inv_l = 1.f / l;
-        uint8_t* orow = args.o + (sp->row0 + t * args.tile_tok + rtok) * args.o_row_stride +
-                        (sp->g * args.G + (row - rtok * args.G)) * args.o_head_stride;
+        uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + rtok) * args.o_row_stride +
+                        (sg.g * args.G + (row - rtok * args.G)) * args.o_head_stride;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
@@ -1144,10 +1152,10 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       if (cut) {
         // published at once; if the others were there before it, its merge waits for the run's end
         mbar_arrive(bar(pbPiece));
-        if (tid < 160) {
-          const bool all = publish_piece(args, *sp, bar(pbPiece), stop);
+        if (tid >= 352) {  // (a warp of tile B: of a lone tile's segment, one with nothing else to do)
+          const bool all = publish_piece(args, sg, bar(pbPiece), stop);
           if (lane == 0) {
-            *reinterpret_cast<PSeg*>(bgen + kOffFirst) = *sp;
+            *reinterpret_cast<PSeg*>(bgen + kOffFirst) = sg;
             decisions[0] = all ? 1u : 0u;
             mbar_arrive(bar(pbDecided));
           }
@@ -1163,7 +1171,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     // where the pieces are few.  Else the piece is stored and published, and merged if all are
     // there then.
     if (open && run) {
-      const PSeg& sg = *seg_at(sidx);
+      const PSeg sg = read_seg(segs + (sidx % kSegQ) * 64);
       const int t = warp >= 8 ? 1 : 0, row = threadIdx.x & 127;
       const int ntok = t ? sg.tokB : sg.tokA;
       const bool active = (st & kLater) != 0;
@@ -1184,7 +1192,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       ok = wait_bounded(bar(pbEarly), 0, stop) && ok;
       if (__all_sync(0xffffffffu, ok)) {
         const bool early = decisions[2] != 0u;
-        if (early && sg.c_last - sg.c_first < kFewPieces) {
+        if (early && sg.c_last - sg.c_first == 1) {
           if (st & kLive)
             merge_with_own<D, BF16>(args, sg, t, row, ocol, active, valid, f, l);
           if (warp == 4) clear_flags(args, sg);
@@ -1211,7 +1219,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     if (st & kFirstCut) {
       const bool ok = wait_bounded(bar(pbDecided), 0, stop);
       if (__all_sync(0xffffffffu, ok) && decisions[0] != 0u) {
-        const PSeg& sg = *reinterpret_cast<const PSeg*>(bgen + kOffFirst);
+        const PSeg sg = read_seg(bar0 + kOffFirst);
         merge_pieces<D, BF16>(args, sg);
         if (warp == 4) clear_flags(args, sg);
       }
