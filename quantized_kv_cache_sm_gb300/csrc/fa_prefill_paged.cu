@@ -661,8 +661,12 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
           s->nbB = tokB > 0 ? w.nb : 0;
           s->j0 = j0;
           s->j1 = j1;
-          w.pieces(plan, cta, s->c_first, s->c_last, s->slot_first);
-          s->own_slot = s->c_first == cta ? s->slot_first : 0;
+          int c_first, c_last, slot_first;
+          w.pieces(plan, cta, c_first, c_last, slot_first);
+          s->c_first = c_first;
+          s->c_last = c_last;
+          s->slot_first = slot_first;
+          s->own_slot = c_first == cta ? slot_first : 0;
           mbar_arrive(bar(pbSegFull + sidx % kSegQ));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;

@@ -358,3 +358,84 @@ def test_every_scale_is_dequantized_as_read(fa, dtype, D):
     for k in (keys, zeros.cuda()):
         assert torch.equal(fa.fa_prefill_paged(q, k, pool, table, starts, lens), want)
     assert fa.fa_get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("kf,vf", [("dense", "dense"), ("q4_0", "q4_0"), ("dense", "q4_0")])
+def test_rows_of_no_sequence_may_hold_anything(fa, kf, vf):
+    """NaN and infinities in q's rows before, behind and (an unused head's place) beside the batch:
+    tiles load some of them along with a sequence's rows."""
+    new, lens = [70, 1, 33], [900, 1500, 33]
+    r = make_ragged(new, lens, 2, 128, 64, "f16", kf, vf, seed=141, first_row=5)
+    rows = 5 + sum(new) + 40
+    q = make_q(rows, 6, 128, "f16", seed=142)
+    clean = fa.fa_prefill_paged(q.cuda(), r.pool(fa, "k"), r.pool(fa, "v"), *r.batch())
+    bad = q.clone()
+    bad[:5], bad[5 + sum(new):] = float("nan"), float("inf")
+    wide = torch.full((rows, 8, 128), float("nan"), dtype=torch.float16)
+    wide[:, 1:7] = bad
+    o = fa.fa_prefill_paged(wide.cuda()[:, 1:7], r.pool(fa, "k"), r.pool(fa, "v"), *r.batch())
+    assert fa.fa_get_status() == fa.FA_OK
+    check(r, q, o.cpu())
+    assert torch.equal(o, clean)
+
+
+def test_calls_on_several_streams_at_once(fa):
+    """Batches of different shapes in flight together, each with scratch of its own."""
+    jobs = []
+    for i, (new, lens, kf) in enumerate([([300, 1], [5000, 3000], "dense"), ([1] * 6, [2500] * 6, "q4_0"),
+                                         ([90, 90], [4000, 90], "q4_0")]):
+        r = make_ragged(new, lens, 8, 128, 128, "f16", kf, kf, seed=151 + i)
+        args = (make_q(sum(new), 32, 128, "f16", seed=161 + i).cuda(), r.pool(fa, "k"),
+                r.pool(fa, "v"), *r.batch())
+        jobs.append((args, fa.fa_prefill_paged(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        outs = [fa.fa_prefill_paged(*args, stream=s) for args, _, s in jobs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o, (_, want, _) in zip(outs, jobs))
+    assert fa.fa_get_status() == fa.FA_OK
+
+
+def test_append_attend_and_read_as_a_server_does(fa):
+    """Prompts, then steps of one and of several tokens, written into q4_0 and dense pools and
+    attended from them, pages handed out as the sequences grow; what was attended is what is read
+    back."""
+    Hq, Hkv, D, page, B = 8, 2, 64, 32, 3
+    g = torch.Generator().manual_seed(171)
+    shape = (40, Hkv, page, D)
+    pools = {"k": fa.Q4Tensor(q4_buffer(torch.zeros(shape, dtype=torch.float16)).cuda(), *shape),
+             "v": torch.full(shape, float("nan"), dtype=torch.float16, device="cuda")}
+    free = torch.randperm(shape[0], generator=g).tolist()
+    table = torch.zeros(B, 12, dtype=torch.int32)
+    lens, held = [0] * B, [0] * B
+    for new in ([70, 33, 1], [1, 1, 1], [1, 4, 0], [5, 1, 100], [1, 1, 1]):
+        lens = [a + b for a, b in zip(lens, new)]
+        for b in range(B):
+            while held[b] * page < lens[b]:
+                table[b, held[b]] = free.pop()
+                held[b] += 1
+        batch = (table.cuda(), torch.tensor([sum(new[:i]) for i in range(B + 1)], dtype=torch.int32,
+                                            device="cuda"),
+                 torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        q, k_new, v_new = (torch.randn(sum(new), h, D, generator=g).half().cuda()
+                           for h in (Hq, Hkv, Hkv))
+        fa.fa_append_paged(k_new, v_new, pools["k"], pools["v"], *batch)
+        o = fa.fa_prefill_paged(q, pools["k"], pools["v"], *batch)
+        # every sequence taken out of the pages whole, then attended in 64 bits
+        whole = (batch[0], torch.tensor([sum(lens[:i]) for i in range(B + 1)], dtype=torch.int32,
+                                        device="cuda"), batch[2])
+        keys, values = (torch.empty(sum(lens), Hkv, D, dtype=torch.float16, device="cuda")
+                        for _ in "kv")
+        fa.fa_read_paged(pools["k"], pools["v"], *whole, keys, values)
+        assert fa.fa_get_status() == fa.FA_OK
+        at = row = 0
+        for b in range(B):
+            if new[b]:
+                rows = slice(row, row + new[b])
+                assert torch.equal(values[at + lens[b] - new[b]:at + lens[b]], v_new[rows])
+                kk, vv = (np64(x[at:at + lens[b]]).transpose(1, 0, 2)[None] for x in (keys, values))
+                want = oracle.attention(np.ascontiguousarray(np64(q[rows]).transpose(1, 0, 2)[None]),
+                                        np.ascontiguousarray(kk), np.ascontiguousarray(vv),
+                                        causal=True, q_pos_offset=lens[b] - new[b], scale=D ** -0.5)
+                check_close(np64(o[rows]), want[0].transpose(1, 0, 2), "f16", f"step {new}, {b}")
+            at, row = at + lens[b], row + new[b]
