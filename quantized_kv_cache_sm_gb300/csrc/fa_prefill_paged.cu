@@ -266,7 +266,7 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
   }
 }
 
-// The same for a thread's own row of a unit of two pieces, the own one still in tensor memory: 64
+// The same for a thread's own row of a unit of two pieces, the own one still in tensor memory: all
 // columns of the other one's in flight.  The pieces are joined in CTA order with the arithmetic of
 // merge_pieces, so that the result does not depend on which CTA came last.
 template <int D, bool BF16>
@@ -276,17 +276,13 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
   const bool own_first = sg.c_first == static_cast<int>(blockIdx.x);
   const float* p = piece_tile<D>(args.part, own_first ? sg.c_last : sg.c_first,
                                  own_first ? 0 : sg.slot_first, t) + row;
-  float v[2][32];
-  auto load = [&](float(&to)[32], int k) {
-    if (valid && k < D) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) to[i] = __ldcg(p + (k + i) * kBM);
-    }
-  };
   const float fo = valid ? __ldcg(p + D * kBM) : -INFINITY;
   const float lo = valid ? __ldcg(p + (D + 1) * kBM) : 0.f;
-  load(v[0], 0);
-  load(v[1], 32);
+  float v[D];
+  if (valid) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) v[i] = __ldcg(p + i * kBM);
+  }
   if (!active) f = -INFINITY;
   const float F = fmaxf(f, fo);
   const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O is not a number
@@ -301,35 +297,29 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
   const int tok = row / args.G;
   uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
                   (sg.g * args.G + (row - tok * args.G)) * args.o_head_stride;
-#pragma unroll 1
-  for (int k0 = 0; k0 < D; k0 += 64) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int k = k0 + 32 * half;
-      uint32_t r[32];
-      __syncwarp();  // the loads from tensor memory are the whole warp's
-      if (active) {
-        tmem_ld32(ocol + k, r);
-        tmem_wait_ld();
-        reg_fence32(r);
-      }
-      float acc[32];
+  for (int k = 0; k < D; k += 32) {
+    uint32_t r[32];
+    __syncwarp();  // the loads from tensor memory are the whole warp's
+    if (active) {
+      tmem_ld32(ocol + k, r);
+      tmem_wait_ld();
+      reg_fence32(r);
+    }
+    uint32_t pk[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float a = w != 0.f ? __uint_as_float(r[i]) : 0.f;
-        const float b = wo != 0.f ? v[half][i] : 0.f;
-        acc[i] = own_first ? fmaf(wo, b, fmaf(w, a, 0.f)) : fmaf(w, a, fmaf(wo, b, 0.f));
-      }
-      load(v[half], k + 64);
-      uint32_t pk[16];
+    for (int i = 0; i < 32; ++i) {
+      const float a = w != 0.f ? __uint_as_float(r[i]) : 0.f;
+      const float b = wo != 0.f ? v[k + i] : 0.f;
+      v[k + i] = own_first ? fmaf(wo, b, fmaf(w, a, 0.f)) : fmaf(w, a, fmaf(wo, b, 0.f));
+    }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      if (valid) {
+    for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(v[k + 2 * e] * inv, v[k + 2 * e + 1] * inv);
+    if (valid) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(orow + 2 * k)[i] =
-              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-      }
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(orow + 2 * k)[i] =
+            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
     }
   }
 }
