@@ -663,6 +663,17 @@ def _paged_pools(k_pages, v_pages, dtype):
     return kf, vf, shape, kt, vt
 
 
+def _here(first, *rest) -> int:
+    """_on_device for plain tensors (None skipped)."""
+    device = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != device:
+            return _on_device(first, *rest)
+    if device < 0 or device != torch._C._cuda_getDevice():
+        return _on_device(first, *rest)
+    return device
+
+
 def _launch_stream(stream, device: int) -> int:
     """_stream for a call whose tensors were found on `device`, the current one: torch's current
     stream there without the Python object around it (0.1 for 2.9 us)."""
@@ -684,7 +695,7 @@ def _paged_rows(append, k, v, k_pages, v_pages, block_table, row_starts, seq_len
     if v is not None:
         vp, vrs, vhs = _packed(v, "V rows", dtype, Hkv, D, rows)
         pv = vt.data_ptr()
-    device = _on_device(k, v, kt, vt, block_table, row_starts, seq_lens)
+    device = _here(k, v, kt, vt, block_table, row_starts, seq_lens)
     shared = (block_table.data_ptr(), row_starts.data_ptr(), seq_lens.data_ptr(), B, rows, Hkv, D,
               NP, page, pps, krs, khs, vrs, vhs, dt, kf, vf, _launch_stream(stream, device))
     lib = load()
@@ -746,7 +757,7 @@ def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tenso
             o = torch.zeros((rows, Hq, D), dtype=dtype, device=q.device)
     qp, qrs, qhs = _packed(q, "q", dtype, Hq, D, rows)
     op, ors, ohs = _packed(o, "o", dtype, Hq, D, rows)
-    device = _on_device(q, kt, vt, o, block_table, row_starts, seq_lens, workspace)
+    device = _here(q, kt, vt, o, block_table, row_starts, seq_lens, workspace)
     lib = load()
     if workspace is None:
         need = max(lib.fa_prefill_paged_workspace_bytes(Hq, Hkv, D), 16)
