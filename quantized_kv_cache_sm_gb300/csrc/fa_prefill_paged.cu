@@ -26,6 +26,14 @@
 //    and its box's are cleared in shared memory, so that what an unused slot holds (NaN included)
 //    never meets a zero weight.  q4_0 rows past the end get a zero scale.
 //
+// What bounds it, measured on one GB300 (GQA 32/8, D = 128; us a call from a CUDA graph): long chunks
+// by each tile's softmax and hand-offs behind the other tile's MMAs, 2048 tokens at the end of 16384
+// f16 keys 328 (1570 TFLOP/s, tensor pipe active 66 %), over q4_0 pools 392, where the dequant takes
+// issue slots and shared-memory bandwidth; single tokens over dense pools by HBM, 64 sequences of
+// 8192 bf16 keys 333 (6.4 TB/s); over q4_0 pools by the lone tile's block step (dequant and operand
+// reads in shared memory, 1.3 us with f16, 1.5 with bf16), the same batch 339; small calls by the 13
+// us of launch, plan, first loads and merges.
+//
 // Warp roles: as in fa_prefill.cu (0 producer and scheduler, 1 TMEM and MMA issuer, 2-3 and 12-15
 // q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B).
 #include <limits.h>
