@@ -271,7 +271,8 @@ fa_status fa_read_paged(const void* k_pages, const void* v_pages, void* k_out, v
  *              sequence) gives zeros; o may not overlap q
  *  D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, page_size a multiple of 16.
  *  A tile of a page outside the pool reads as zeros (recorded, see above).  What the pools hold past
- *  a sequence's end does not matter, NaN included.
+ *  a sequence's end does not matter, NaN included; a NaN or an infinity in a key or value of the
+ *  sequence itself may reach any of its rows, those before that position too (a zero weight times it).
  *  workspace : >= fa_prefill_paged_workspace_bytes(Hq, Hkv, D) bytes on the current device, contents
  *              on entry irrelevant, not shared by calls in flight at the same time (see fa_fwd_ex) */
 size_t fa_prefill_paged_workspace_bytes(int Hq, int Hkv, int D);

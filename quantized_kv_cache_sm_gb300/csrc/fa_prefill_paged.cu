@@ -536,11 +536,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         if (!w) return false;
         const int r1 = (r0 + args.box - 1) & -args.box;
         uint8_t* p = sgen + (stage - sbase);
-        for (int i = lane; i < (r1 - r0) * kChunks * 8; i += 32) {
-          const int c = i / ((r1 - r0) * 8), k = i - c * ((r1 - r0) * 8);
-          *reinterpret_cast<uint4*>(p + c * (kBN * 128) + r0 * 128 + k * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
+        for (int i = lane; i < (r1 - r0) * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            *reinterpret_cast<uint4*>(p + c * (kBN * 128) + r0 * 128 + i * 16) =
+                make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         ++tails;
