@@ -194,7 +194,7 @@ def _check_q4(t: Q4Tensor, what: str):
     """A Q4Tensor's buffer must be one contiguous uint8 vector holding both planes."""
     if t.buf.dtype != torch.uint8 or t.buf.dim() != 1 or not t.buf.is_contiguous():
         raise ValueError(f"{what}: the q4_0 buffer must be a contiguous uint8 vector")
-    need = _q4_0_bytes(t.B, t.H, t.S, t.D)
+    need = _q4_0_bytes(int(t.B), int(t.H), int(t.S), int(t.D))
     if need == 0 or t.buf.numel() < need:
         raise ValueError(f"{what}: a q4_0 tensor of shape {t.shape} needs {need} bytes, "
                          f"its buffer holds {t.buf.numel()}")
@@ -296,12 +296,12 @@ def fa_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, q_pos_offset, causal) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _q4_0_bytes(B: int, H: int, S: int, D: int) -> int:
-    return int(load().fa_q4_0_bytes(int(B), int(H), int(S), int(D)))
+    return int(load().fa_q4_0_bytes(B, H, S, D))
 
 
 def fa_q4_0_bytes(B, H, S, D) -> int:
     # a pure function of the shape, asked on every call that takes a q4_0 tensor: cached
-    return _q4_0_bytes(B, H, S, D)
+    return _q4_0_bytes(int(B), int(H), int(S), int(D))
 
 
 def fa_q4_0_scale_offset(B, H, S, D) -> int:
