@@ -45,6 +45,7 @@ __device__ __forceinline__ bool locate_rows(const PagedBatch& b, int Hkv, int t0
   __shared__ int32_t s_lens[kSmemSeqs];
   const int tid = threadIdx.x;
   const bool small = b.B <= kSmemSeqs;
+  const int64_t cap = static_cast<int64_t>(b.page_size) * b.pages_per_seq;
   int bad = 0;
   for (int i = tid; i < b.B; i += kThreads) {
     const int v = __ldg(b.starts + i), next = __ldg(b.starts + i + 1);
@@ -70,10 +71,8 @@ __device__ __forceinline__ bool locate_rows(const PagedBatch& b, int Hkv, int t0
         const int mid = (lo + hi) >> 1;
         if (starts[mid] <= t) lo = mid; else hi = mid;
       }
-      const int len = lens[lo];
-      const int64_t cap = static_cast<int64_t>(b.page_size) * b.pages_per_seq;
-      const int pos = len - (starts[lo + 1] - t);
-      if (pos >= 0 && len <= cap) {
+      const int pos = row_position(lens[lo], cap, starts[lo + 1] - t);
+      if (pos >= 0) {
         const int lp = pos / b.page_size;
         const int page = __ldg(b.table + static_cast<int64_t>(lo) * b.pages_per_seq + lp);
         if (page >= 0 && page < b.num_pages)

@@ -24,6 +24,17 @@ __host__ __device__ __forceinline__ bool bad_start(int v, int next, int rows) {
   return v < 0 || next < v || next > rows;
 }
 
+// a length of a sequence that the block table cannot hold
+__host__ __device__ __forceinline__ bool bad_length(int len, int64_t cap) {
+  return len < 0 || len > cap;
+}
+// position of the row that is `back` rows before its sequence's end (1: the last row); negative
+// where it has none: a bad length, or more rows than tokens.  (The length is looked at first: near
+// -2^31 the difference would overflow to a large position.)
+__host__ __device__ __forceinline__ int row_position(int len, int64_t cap, int back) {
+  return bad_length(len, cap) ? -1 : len - back;
+}
+
 // x / d for 0 <= x < 2^31 by a multiplication and a shift: with s = ceil(log2 d) and m =
 // floor(2^32 (2^s - d) / d) + 1, x / d = (mulhi(m, x) + x) >> s (Granlund and Montgomery, "Division
 // by invariant integers using multiplication", PLDI 1994)

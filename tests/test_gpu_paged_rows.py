@@ -308,3 +308,27 @@ def test_rows_and_heads_split_over_ctas(fa, Hkv, D, rows):
     assert fa.fa_get_status() == fa.FA_OK
     assert torch.equal(stored(k), bits(after_append(r, "k", k_new)))
     assert torch.equal(stored(v), bits(after_append(r, "v", v_new)))
+
+
+@pytest.mark.parametrize("fmt", ["dense", "q4_0"])
+def test_lengths_at_the_ends_of_32_bits(fa, fmt):
+    """Every length that the table cannot hold is reported and its rows skipped, down to -2^31, from
+    which a row's place is no longer a difference of 32 bits; the other sequence is written and read."""
+    Hkv, D, page = 2, 64, 8
+    r = make_ragged([4, 3], [20, 11], Hkv, D, page, "f16", fmt, fmt, seed=2)
+    x = torch.randn(7, Hkv, D, generator=torch.Generator().manual_seed(7)).half()
+    table, starts, _ = r.batch()
+    only = make_ragged([4, 3], [20, 11], Hkv, D, page, "f16", fmt, fmt, seed=2)
+    only.new = [0, 3]
+    only.starts = torch.tensor([4, 4, 7], dtype=torch.int32)
+    want = bits(after_append(only, "k", x))
+    for n in (-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 3, -2 ** 31 + 4, -1, 2 ** 31 - 1, 2 ** 30):
+        lens = torch.tensor([n, 11], dtype=torch.int32, device="cuda")
+        k, v = r.pool(fa, "k"), r.pool(fa, "v")
+        out = torch.full((7, Hkv, D), 7.0, dtype=torch.float16, device="cuda")
+        fa.fa_append_paged(x.cuda(), x.cuda(), k, v, table, starts, lens)
+        assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
+        fa.fa_read_paged(k, None, table, starts, lens, out)
+        assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
+        assert torch.equal(stored(k), want), n
+        assert (out[:4] == 7.0).all() and (out[4:] != 7.0).any()
