@@ -332,3 +332,25 @@ def test_lengths_at_the_ends_of_32_bits(fa, fmt):
         assert fa.fa_get_status() == fa.FA_ERR_INVALID_ARG
         assert torch.equal(stored(k), want), n
         assert (out[:4] == 7.0).all() and (out[4:] != 7.0).any()
+
+
+@pytest.mark.parametrize("B", [3, 1500])
+def test_bad_length_of_a_sequence_without_rows_is_reported(fa, B):
+    """In a batch that fits shared memory and in a larger one; the rows of the others are moved."""
+    Hkv, D, page = 1, 64, 16
+    pool = torch.zeros(4, Hkv, page, D, dtype=torch.float16, device="cuda")
+    x = torch.randn(2, Hkv, D, generator=torch.Generator().manual_seed(8)).half().cuda()
+    table = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    table[0], table[B - 1] = torch.tensor([1, 2]), torch.tensor([3, 0])
+    starts = torch.ones(B + 1, dtype=torch.int32, device="cuda")
+    starts[0], starts[B] = 0, 2
+    for n in (0, 33, -1, -2 ** 31):
+        lens = torch.full((B,), 32, dtype=torch.int32, device="cuda")
+        lens[B // 2] = n
+        status = fa.FA_OK if n == 0 else fa.FA_ERR_INVALID_ARG
+        out = torch.empty_like(x)
+        fa.fa_append_paged(x, None, pool, None, table, starts, lens)
+        assert fa.fa_get_status() == status
+        fa.fa_read_paged(pool, None, table, starts, lens, out)
+        assert fa.fa_get_status() == status
+        assert torch.equal(out, x)
