@@ -331,8 +331,13 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
     }
   }
 }
+// Publication flag of CTA c's piece: its slot is slot_first for the unit's first CTA, 0 for the others,
+// and the address stays within CTA c's two flags whatever the segment holds.
+__device__ __forceinline__ uint32_t* flag_at(const PArgs& args, int c, int slot) {
+  return args.pflags + 2 * c + (slot & 1);
+}
 __device__ __forceinline__ uint32_t* piece_flag(const PArgs& args, const PSeg& sg, int c) {
-  return args.pflags + 2 * c + (c == sg.c_first ? sg.slot_first : 0);
+  return flag_at(args, c, sg.slot_first & -static_cast<int>(c == sg.c_first));
 }
 // whether all pieces but CTA `but`'s (-1: all pieces) are published, by one warp; their rows may be
 // read after it
@@ -380,7 +385,7 @@ __device__ __forceinline__ bool publish_piece(const PArgs& args, const PSeg& sg,
                                               uint32_t stop) {
   if (!__all_sync(0xffffffffu, wait_bounded(stored, 0, stop))) return false;
   if ((threadIdx.x & 31) == 0)
-    st_release_gpu(args.pflags + 2 * static_cast<int>(blockIdx.x) + sg.own_slot, args.tag);
+    st_release_gpu(flag_at(args, static_cast<int>(blockIdx.x), sg.own_slot), args.tag);
   __syncwarp();
   fence_sc_gpu();
   return pieces_there(args, sg, -1);

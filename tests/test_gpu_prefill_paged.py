@@ -439,3 +439,28 @@ def test_append_attend_and_read_as_a_server_does(fa):
                                         causal=True, q_pos_offset=lens[b] - new[b], scale=D ** -0.5)
                 check_close(np64(o[rows]), want[0].transpose(1, 0, 2), "f16", f"step {new}, {b}")
             at, row = at + lens[b], row + new[b]
+
+
+@pytest.mark.parametrize("D,kf,vf", [(64, "dense", "q4_0"), (64, "q4_0", "q4_0"), (128, "q4_0", "dense"),
+                                     (128, "q4_0", "q4_0"), (128, "dense", "dense")])
+def test_nothing_beside_the_workspace_and_the_rows_is_written(fa, D, kf, vf):
+    """Guard bytes around the scratch and around o's rows, over many launches of a batch whose units are
+    cut: its prompts' units begin at token 512 among others."""
+    r = make_ragged([333, 1, 1021, 77, 600], [333, 1, 1021, 77, 600], 8, D, 128, "f16", kf, vf, seed=181)
+    n = sum(r.new)
+    q = make_q(n, 8, D, "f16", seed=182).cuda()
+    k, v, batch = r.pool(fa, "k"), r.pool(fa, "v"), r.batch()
+    need, guard = fa.fa_prefill_paged_workspace_bytes(8, 8, D), 1 << 20
+    scratch = torch.full((need + 2 * guard,), 90, dtype=torch.uint8, device="cuda")
+    ws = scratch[guard:guard + need]
+    rows = torch.full((n + 64, 8, D), 7.0, dtype=torch.float16, device="cuda")
+    o = rows[32:32 + n]
+    want = fa.fa_prefill_paged(q, k, v, *batch)
+    check(r, q.cpu(), want.cpu())
+    for _ in range(300):
+        o.fill_(7.0)
+        fa.fa_prefill_paged(q, k, v, *batch, o, workspace=ws)
+        assert torch.equal(o, want)
+    assert fa.fa_get_status() == fa.FA_OK
+    assert (scratch[:guard] == 90).all() and (scratch[guard + need:] == 90).all()
+    assert (rows[:32] == 7.0).all() and (rows[32 + n:] == 7.0).all()
