@@ -346,7 +346,10 @@ __device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, 
   for (int c = sg.c_first + (threadIdx.x & 31); c <= sg.c_last; c += 32)
     all = all && (c == but || ld_relaxed_gpu(piece_flag(args, sg, c)) == args.tag);
   all = __all_sync(0xffffffffu, all);
-  if (all) fence_acq_rel_gpu();
+  if (all) {
+    fence_acq_rel_gpu();  // each lane acquires the pieces whose flags it has read,
+    __syncwarp();         // all before the lane that tells the other warps
+  }
   return all;
 }
 
