@@ -274,16 +274,15 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
   }
 }
 
-// The same for a thread's own row of a unit of two pieces, the own one still in tensor memory: all
-// columns of the other one's in flight.  The pieces are joined in CTA order with the arithmetic of
-// merge_pieces, so that the result does not depend on which CTA came last.
+// The same for a thread's own row of a unit of two pieces, where this CTA began the unit and the other
+// piece is published: the own one still in tensor memory, all columns of the other one's in flight.
+// Joined in CTA order with the arithmetic of merge_pieces, so that the result does not depend on which
+// CTA came last.
 template <int D, bool BF16>
 __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg, int t, int row,
                                                uint32_t ocol, bool active, bool valid, float f,
                                                float l) {
-  const bool own_first = sg.c_first == static_cast<int>(blockIdx.x);
-  const float* p = piece_tile<D>(args.part, own_first ? sg.c_last : sg.c_first,
-                                 own_first ? 0 : sg.slot_first, t) + row;
+  const float* p = piece_tile<D>(args.part, sg.c_last, 0, t) + row;
   const float fo = valid ? __ldcg(p + D * kBM) : -INFINITY;
   const float lo = valid ? __ldcg(p + (D + 1) * kBM) : 0.f;
   float v[D];
@@ -296,11 +295,8 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
   const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O is not a number
   const float wo = fo == -INFINITY ? 0.f : ex2(fo - F);
   float L = 0.f;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const bool mine = (c == 0) == own_first;
-    if ((mine ? w : wo) != 0.f) L = fmaf(mine ? w : wo, mine ? l : lo, L);
-  }
+  if (w != 0.f) L = fmaf(w, l, L);
+  if (wo != 0.f) L = fmaf(wo, lo, L);
   const float inv = F == -INFINITY ? 0.f : 1.f / L;
   const int tok = row / args.G;
   uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + tok) * args.o_row_stride +
@@ -316,13 +312,16 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
     }
     uint32_t pk[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float a = w != 0.f ? __uint_as_float(r[i]) : 0.f;
-      const float b = wo != 0.f ? v[k + i] : 0.f;
-      v[k + i] = own_first ? fmaf(wo, b, fmaf(w, a, 0.f)) : fmaf(w, a, fmaf(wo, b, 0.f));
-    }
+    for (int e = 0; e < 16; ++e) {
+      float x[2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(v[k + 2 * e] * inv, v[k + 2 * e + 1] * inv);
+      for (int i = 0; i < 2; ++i) {
+        const float a = w != 0.f ? __uint_as_float(r[2 * e + i]) : 0.f;
+        const float b = wo != 0.f ? v[k + 2 * e + i] : 0.f;
+        x[i] = fmaf(wo, b, fmaf(w, a, 0.f)) * inv;
+      }
+      pk[e] = pack2<BF16>(x[0], x[1]);
+    }
     if (valid) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
