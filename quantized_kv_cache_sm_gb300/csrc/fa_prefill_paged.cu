@@ -174,10 +174,11 @@ template <>
 struct DqOf<true> {
   using type = DqSplit;
 };
-// A segment out of shared memory, whole and unconditionally.  (Fields read one by one where they were
-// needed left it to the compiler to read some of them under a condition, and in the layout with q4_0
-// sides such a selection, `own CTA first ? slot_first : 0`, now and then gave 512 for 0 to a whole
-// warp, whose rows then went outside the workspace.  No build that reads them unconditionally did.)
+// A segment out of shared memory, whole and unconditionally.  (Builds that moved registers from the other
+// warps to the softmax warps, as fa_prefill.cu does, and left it to the compiler to read some fields
+// under a condition, now and then saw 512 for 0 in the selection `own CTA first ? slot_first : 0`, a
+// whole warp at a time, whose rows then went outside the workspace.  Why is not known.  Builds without
+// either were clean; this one has neither.)
 __device__ __forceinline__ int4 lds_int4(uint32_t addr) {
   int4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -196,6 +197,153 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(src_bytes)
                : "memory");
+}
+
+// softmax_block in fewer registers, for the sixteen-warp layout's 128 a thread.  A block that every row of
+// the warp sees whole is read 64 keys at a time, the second 64 under way while the first are turned into
+// P.  The first half's P stays packed in registers until the second half's scores are there and their
+// max shows, with the first half's row sum (see kSumTrigger), that no row of the warp needs the frame
+// test; from then on P goes over S as it is formed.  Otherwise -- a row's first block, a masked one, or
+// one that needs the test -- S is whole still and is read twice: for the block's max, and to form P in
+// the frame that follows.  Frames, P and sums are those of softmax_block to the bit.
+//
+// (softmax_block's 128 scores in registers need 168 of them a thread, which sixteen warps have only
+// where the other warps hand theirs over.  Measured against that, us: 16 x 5 draft tokens over q4_0
+// 47.0 -> 45.8, five prompts with q4_0 V 19.0 -> 20.7, 2048 tokens at 16384 q4_0 keys 396 -> 416.  Other
+// forms within 128 registers on the same three: all of P kept until the row sum is known 46.9 / 19.6 /
+// 431, three quarters of it 45.5 / 20.8 / 422, a short form for masked blocks too 50.4 / 20.3 / 420, the
+// max first for every block 50.5 / 20.6 / 476.)
+template <bool MASK>
+__device__ __forceinline__ void mask_chunk(uint32_t (&r)[32], int c, int rel_lim) {
+  if (MASK) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (32 * c + i > rel_lim) r[i] = __float_as_uint(-INFINITY);
+  }
+}
+__device__ __forceinline__ float max_chunk(const uint32_t (&r)[32]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) m = fmax3(m, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+  return m;
+}
+struct RowSum {
+  uint64_t acc0, acc1;
+};
+template <bool BF16>
+__device__ __forceinline__ void exp_chunk(const uint32_t (&r)[32], uint32_t (&p)[16], uint64_t sl2x2,
+                                          uint64_t nfx2, RowSum& s) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 t = f2_unpack(f2_fma(
+        f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sl2x2, nfx2));
+    const float p0 = ex2(t.x), p1 = ex2(t.y);
+    const uint64_t pp = f2_pack(p0, p1);
+    if (i & 1) s.acc1 = f2_add(s.acc1, pp); else s.acc0 = f2_add(s.acc0, pp);
+    p[i] = pack2<BF16>(p0, p1);
+  }
+}
+__device__ __forceinline__ float row_sum(const RowSum& s) {
+  const float2 a = f2_unpack(f2_add(s.acc0, s.acc1));
+  return a.x + a.y;
+}
+__device__ __forceinline__ void load_chunk(uint32_t scol, int c, uint32_t (&r)[32]) {
+  tmem_ld32(scol + 32 * c, r);
+}
+// P in frame f over S unless a row needs the frame test (then nothing is stored): the row sum
+template <bool BF16>
+__device__ __forceinline__ bool exp_in_frame(uint32_t scol, float sl2, float f, float& sum) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2), nfx2 = f2_pack(-f, -f);
+  RowSum acc = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+  uint32_t r0[32], r1[32], r2[32], r3[32], p0[16], p1[16];
+  load_chunk(scol, 0, r0);
+  load_chunk(scol, 1, r1);
+  tmem_wait_ld();
+  reg_fence32(r0);
+  reg_fence32(r1);
+  exp_chunk<BF16>(r0, p0, sl2x2, nfx2, acc);
+  load_chunk(scol, 2, r2);
+  exp_chunk<BF16>(r1, p1, sl2x2, nfx2, acc);
+  load_chunk(scol, 3, r3);
+  tmem_wait_ld();
+  reg_fence32(r2);
+  reg_fence32(r3);
+  const float m = fmaxf(max_chunk(r2), max_chunk(r3)) * sl2;
+  if (__any_sync(0xffffffffu, row_sum(acc) > kSumTrigger || m > f + kMarginLog2)) return false;
+  tmem_st16(scol, p0);
+  tmem_st16(scol + 16, p1);
+  exp_chunk<BF16>(r2, p0, sl2x2, nfx2, acc);
+  tmem_st16(scol + 32, p0);
+  exp_chunk<BF16>(r3, p1, sl2x2, nfx2, acc);
+  tmem_st16(scol + 48, p1);
+  sum = row_sum(acc);
+  return true;
+}
+template <bool MASK>
+__device__ __forceinline__ float block_max(uint32_t scol, int rel_lim) {
+  float m[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    load_chunk(scol, c, r);
+    tmem_wait_ld();
+    reg_fence32(r);
+    mask_chunk<MASK>(r, c, rel_lim);
+    m[c] = max_chunk(r);
+  }
+  return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+// P in frame f over S, P of keys 32 c .. over S of keys 16 c .., which are read by then: the row sum
+template <bool MASK, bool BF16>
+__device__ __forceinline__ float exp_block(uint32_t scol, int rel_lim, float sl2, float f) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2), nfx2 = f2_pack(-f, -f);
+  RowSum acc = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32], p[16];
+    load_chunk(scol, c, r);
+    tmem_wait_ld();
+    reg_fence32(r);
+    mask_chunk<MASK>(r, c, rel_lim);
+    exp_chunk<BF16>(r, p, sl2x2, nfx2, acc);
+    tmem_st16(scol + 16 * c, p);
+  }
+  return row_sum(acc);
+}
+template <int D, bool BF16, class WaitO>
+__device__ __forceinline__ void softmax_block_lean(uint32_t scol, uint32_t ocol, bool need_mask,
+                                                   int rel_lim, float sl2, bool o_live, float& f,
+                                                   float& l, const WaitO& wait_o) {
+  if (!__any_sync(0xffffffffu, f == -INFINITY)) {
+    float sum;
+    if (!need_mask && exp_in_frame<BF16>(scol, sl2, f, sum)) {
+      l += sum;
+      return;
+    }
+  }
+  const float m2 = (need_mask ? block_max<true>(scol, rel_lim) : block_max<false>(scol, rel_lim)) * sl2;
+  const bool need = m2 > f + kMarginLog2;
+  float alpha = 1.f;
+  if (need) {
+    alpha = ex2(f - m2);
+    l *= alpha;
+    f = m2;
+  }
+  if (__any_sync(0xffffffffu, need) && o_live) {
+    wait_o();
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t r[32];
+      tmem_ld32(ocol + 32 * c, r);
+      tmem_wait_ld();
+      reg_fence32(r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+      tmem_st32(ocol + 32 * c, r);
+    }
+  }
+  l += need_mask ? exp_block<true, BF16>(scol, rel_lim, sl2, f)
+                 : exp_block<false, BF16>(scol, rel_lim, sl2, f);
 }
 
 // Merge of one unit's pieces by the 256 softmax threads.  A tile's threads (both tiles' where tile
@@ -275,21 +423,25 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
 }
 
 // The same for a thread's own row of a unit of two pieces, where this CTA began the unit and the other
-// piece is published: the own one still in tensor memory, all columns of the other one's in flight.
+// piece is published: the own one still in tensor memory, FLY columns of the other one's in flight
+// (D, or what 128 registers hold).
 // Joined in CTA order with the arithmetic of merge_pieces, so that the result does not depend on which
 // CTA came last.
-template <int D, bool BF16>
+template <int D, bool BF16, int FLY>
 __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg, int t, int row,
                                                uint32_t ocol, bool active, bool valid, float f,
                                                float l) {
   const float* p = piece_tile<D>(args.part, sg.c_last, 0, t) + row;
   const float fo = valid ? __ldcg(p + D * kBM) : -INFINITY;
   const float lo = valid ? __ldcg(p + (D + 1) * kBM) : 0.f;
-  float v[D];
-  if (valid) {
+  float v[FLY];
+  auto load = [&](int k) {
+    if (valid) {
 #pragma unroll
-    for (int i = 0; i < D; ++i) v[i] = __ldcg(p + i * kBM);
-  }
+      for (int i = 0; i < FLY; ++i) v[i] = __ldcg(p + (k + i) * kBM);
+    }
+  };
+  load(0);
   if (!active) f = -INFINITY;
   const float F = fmaxf(f, fo);
   const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O is not a number
@@ -317,7 +469,7 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float a = w != 0.f ? __uint_as_float(r[2 * e + i]) : 0.f;
-        const float b = wo != 0.f ? v[k + 2 * e + i] : 0.f;
+        const float b = wo != 0.f ? v[k % FLY + 2 * e + i] : 0.f;
         x[i] = fmaf(wo, b, fmaf(w, a, 0.f)) * inv;
       }
       pk[e] = pack2<BF16>(x[0], x[1]);
@@ -328,6 +480,7 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
         reinterpret_cast<uint4*>(orow + 2 * k)[i] =
             make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
     }
+    if ((k + 32) % FLY == 0 && k + 32 < D) load(k + 32);
   }
 }
 // Publication flag of CTA c's piece: its slot is slot_first for the unit's first CTA, 0 for the others,
@@ -507,9 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const bool run = *has_run != 0;
 
-  // registers moved to the softmax warpgroups with a q4_0 side, as in fa_prefill.cu
   if (warp < 4 || warp >= 12) {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 0) {
       // -------------------------------------------------- scheduler and producer
       bool ok = true;
@@ -1016,7 +1167,6 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
     // ---------------------------------------------------------------- softmax rows
     // Registers: a block's 128 scores and little else.  Nothing but the two words below is carried
     // from one segment to the next, and what follows from the thread's number or the segment is
@@ -1089,12 +1239,18 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
               tc_fence_after();
             }
           };
-          int moves = 0;
-          float top = 0.f;
-          softmax_block<D, BF16>(tm + (st & (kSecond | kTileB) ? col_s(1) : col_s(0)),
-                                 tm + (st & kTileB ? C::kColO1 : C::kColO0),
-                                 __any_sync(0xffffffffu, rel < kBN - 1), rel, args.scale_log2,
-                                 (st & kLater) != 0, f, l, moves, top, wait_pv);
+          const uint32_t scol = tm + (st & (kSecond | kTileB) ? col_s(1) : col_s(0));
+          const uint32_t ocol = tm + (st & kTileB ? C::kColO1 : C::kColO0);
+          const bool mask = __any_sync(0xffffffffu, rel < kBN - 1);
+          if constexpr (C::kWide) {
+            softmax_block_lean<D, BF16>(scol, ocol, mask, rel, args.scale_log2, (st & kLater) != 0,
+                                        f, l, wait_pv);
+          } else {
+            int moves = 0;
+            float top = 0.f;
+            softmax_block<D, BF16>(scol, ocol, mask, rel, args.scale_log2, (st & kLater) != 0, f,
+                                   l, moves, top, wait_pv);
+          }
           tmem_wait_st();
         }
         rel -= kBN;
@@ -1203,7 +1359,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         const bool early = decisions[2] != 0u;
         if (early && sg.c_last - sg.c_first == 1) {
           if (st & kLive)
-            merge_with_own<D, BF16>(args, sg, t, row, ocol, active, valid, f, l);
+            merge_with_own<D, BF16, C::kWide ? 64 : D>(args, sg, t, row, ocol, active, valid, f, l);
           if (warp == 4) clear_flags(args, sg);
         } else {
           if (st & kLive) store_piece<D>(args, sg.own_slot, t, row, ocol, active, valid, f, l);
