@@ -126,6 +126,16 @@ __device__ __forceinline__ float* piece_tile(float* part, int c, int slot, int t
   return part + ((static_cast<int64_t>(c) * 2 + (slot & 1)) * 2 + t) * (D + 2) * kBM;
 }
 
+// The last key that a row of the segment sees: tok counts from tile A's first token
+__device__ __forceinline__ int last_key(const PSeg& sg, int causal, int tok) {
+  return causal ? min(sg.len - 1, sg.pos0 + tok) : sg.len - 1;
+}
+// A piece's frame as the merges take it: -inf where the row sees no key of the piece (its sums are not
+// used), +inf where its sum is NaN, so that the merged row is NaN however small the piece's weight.
+__device__ __forceinline__ float piece_frame(bool sees, float f, float l) {
+  return !sees ? -INFINITY : l == l ? f : INFINITY;
+}
+
 // the thread's number, formed anew where it is asked for
 __device__ __forceinline__ int opaque_tid() {
   uint32_t tid;
@@ -349,7 +359,7 @@ __device__ __forceinline__ void softmax_block_lean(uint32_t scol, uint32_t ocol,
 // Merge of one unit's pieces by the 256 softmax threads.  A tile's threads (both tiles' where tile
 // B is absent) are laid out as Rp rows x column groups, Rp the rows in use rounded up to a power of
 // two: a few rows spread over many column groups.  kCols columns of kFly pieces are loaded together
-// and joined with a running frame.  A piece whose row saw no key has frame -inf.
+// and joined with a running frame.  (Frames: piece_frame.)
 template <int D, bool BF16>
 __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) {
   constexpr int kFly = 4, kCols = 16;
@@ -401,7 +411,7 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
 #pragma unroll
       for (int c = 0; c < kFly; ++c) {
         const float w = f[c] == -INFINITY ? 0.f : ex2(f[c] - F);
-        if (w == 0.f) continue;  // (frame -inf: its O is not a number)
+        if (w == 0.f) continue;  // (frame -inf: its O may be no number)
         L = fmaf(w, l[c], L);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) acc[i] = fmaf(w, v[c][i], acc[i]);
@@ -426,7 +436,7 @@ __device__ __forceinline__ void merge_pieces(const PArgs& args, const PSeg& sg) 
 // piece is published: the own one still in tensor memory, FLY columns of the other one's in flight
 // (D, or what 128 registers hold).
 // Joined in CTA order with the arithmetic of merge_pieces, so that the result does not depend on which
-// CTA came last.
+// CTA came last.  f: the own piece's, by piece_frame.
 template <int D, bool BF16, int FLY>
 __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg, int t, int row,
                                                uint32_t ocol, bool active, bool valid, float f,
@@ -442,9 +452,8 @@ __device__ __forceinline__ void merge_with_own(const PArgs& args, const PSeg& sg
     }
   };
   load(0);
-  if (!active) f = -INFINITY;
   const float F = fmaxf(f, fo);
-  const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O is not a number
+  const float w = f == -INFINITY ? 0.f : ex2(f - F);    // 0: the piece's O may be no number
   const float wo = fo == -INFINITY ? 0.f : ex2(fo - F);
   float L = 0.f;
   if (w != 0.f) L = fmaf(w, l, L);
@@ -505,13 +514,12 @@ __device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, 
   return all;
 }
 
-// Store of a thread's row of a piece into one of the CTA's slots
+// Store of a thread's row of a piece into one of the CTA's slots; f by piece_frame
 template <int D>
 __device__ __forceinline__ void store_piece(const PArgs& args, int slot, int t, int row,
                                             uint32_t ocol, bool active, bool valid, float f,
                                             float l) {
   float* pt = piece_tile<D>(args.part, static_cast<int>(blockIdx.x), slot, t) + row;
-  const bool have = active && f != -INFINITY;
   if (active) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
@@ -527,8 +535,8 @@ __device__ __forceinline__ void store_piece(const PArgs& args, int slot, int t, 
     }
   }
   if (valid) {
-    pt[D * kBM] = have ? f : -INFINITY;
-    pt[(D + 1) * kBM] = have ? l : 0.f;
+    pt[D * kBM] = f;
+    pt[(D + 1) * kBM] = l;
   }
 }
 
@@ -1281,10 +1289,14 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         tc_fence_after();
       }
       const bool valid = rtok < ntok && row < args.G * args.tile_tok;
+      // (its first key is in the segment's first block if any is; f alone does not say: a row of NaN
+      // scores leaves it at -inf)
+      const bool sees = last_key(sg, plan.causal, t * args.tile_tok + rtok) >= sg.j0 * kBN;
       if (cut) {  // the last piece of a unit that other CTAs began
-        if (st & kLive) store_piece<D>(args, 0, t, row, ocol, (st & kLater) != 0, valid, f, l);
+        if (st & kLive)
+          store_piece<D>(args, 0, t, row, ocol, (st & kLater) != 0, valid, piece_frame(sees, f, l), l);
       } else if ((st & kLater) && (st & kLive)) {
-        const bool none = f == -INFINITY;  // the row sees no key
+        const bool none = !sees;
         const float inv_l = 1.f / l;
         uint8_t* orow = args.o + (sg.row0 + t * args.tile_tok + rtok) * args.o_row_stride +
                         (sg.g * args.G + (row - rtok * args.G)) * args.o_head_stride;
@@ -1342,6 +1354,9 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       const bool active = (st & kLater) != 0;
       const bool valid = row / args.G < ntok && row < args.G * args.tile_tok;
       const uint32_t ocol = tm + (t ? C::kColO1 : C::kColO0);
+      f = piece_frame(active && last_key(sg, plan.causal, t * args.tile_tok + row / args.G) >=
+                                    sg.j0 * kBN,
+                      f, l);
       bool ok = true;
       if (warp == 4) {
         const bool early = pieces_there(args, sg, cta);

@@ -464,3 +464,49 @@ def test_nothing_beside_the_workspace_and_the_rows_is_written(fa, D, kf, vf):
     assert fa.fa_get_status() == fa.FA_OK
     assert (scratch[:guard] == 90).all() and (scratch[guard + need:] == 90).all()
     assert (rows[:32] == 7.0).all() and (rows[32 + n:] == 7.0).all()
+
+
+NAN_CASES = [(kf, vf, dtype, D)
+             for kf, vf in (("dense", "dense"), ("q4_0", "q4_0"), ("q4_0", "dense"))
+             for dtype, D in (("f16", 128), ("bf16", 64))]
+
+
+@pytest.mark.parametrize("kf,vf,dtype,D", NAN_CASES)
+def test_nan_in_a_row_stays_in_that_row(fa, kf, vf, dtype, D):
+    """A NaN in one query row and head makes that row's output NaN, in whole units and in units cut into two
+    and more pieces; every other row keeps its bits, and rows without keys are zeros whatever they hold."""
+    r = make_ragged([3, 70, 1, 40, 2, 1], [500, 70, 9000, 3000, 1, 0], 2, D, 64, dtype, kf, vf, seed=191)
+    q = make_q(sum(r.new), 8, D, dtype, seed=192)
+    clean = run(fa, r, q)
+    check(r, q, clean.cpu())
+    bad = q.clone()
+    rows = {0: 1, 5: 0, 3 + 69: 7, 73: 2, 74: 3, 74 + 39: 6, 114: 4, 115: 5, 116: 1}
+    for t, h in rows.items():
+        bad[t, h, 5] = float("nan")
+    o = run(fa, r, bad)
+    for t, h in rows.items():
+        seq = int((r.starts[1:] <= t).sum())
+        blind = r.lens[seq] - (int(r.starts[seq + 1]) - t) < 0
+        if blind:
+            assert (o[t, h] == 0).all(), t
+        else:
+            assert torch.isnan(o[t, h]).all(), t
+        o[t, h] = clean[t, h]
+    assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("kf,vf,dtype,D", NAN_CASES)
+@pytest.mark.parametrize("at", [0, 768, 4096, 8960])
+def test_nan_in_a_key_reaches_every_row_that_sees_it(fa, kf, vf, dtype, D, at):
+    """One token over 9000 keys, a unit of many pieces: a key of NaN (a q4_0 key's scales) makes the row NaN
+    whichever piece it lies in, and also where all keys of a piece are NaN."""
+    for width in (1, 128, 1000):
+        r = make_ragged([1], [9000], 1, D, 64, dtype, kf, vf, seed=193)
+        for p in range(at, min(9000, at + width)):
+            page, slot = int(r.table[0, p // 64]), p % 64
+            if kf == "dense":
+                r.k[page, :, slot] = float("nan")
+            else:
+                q4_planes(r.k, r.shape)[1][page, :, slot] = 0x7E00
+        q = make_q(1, 4, D, dtype, seed=194)
+        assert torch.isnan(run(fa, r, q)).all()
