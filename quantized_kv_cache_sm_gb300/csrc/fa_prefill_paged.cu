@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       int pg = 0;     // paired ring: slots filled
       int qn = 0;     // Q loads issued
       int tails = 0;  // V tiles cleared past the sequence's end
+      bool tail_out = false;  // one more is loaded or on its way
       auto box_row = [&](int j) -> int {  // first row in its page of box `lane` of block j
         return PagedWalk::page_row(plan, j * kBN + (lane << args.box_bits));
       };
@@ -699,6 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
       auto clear_tail = [&](uint32_t stage, int r0) -> bool {
         bool w = mbar_wait(bar(pbTail), tails & 1, abort_flag, &g_prefill_paged_error);
         w = __all_sync(0xffffffffu, w);
+        tail_out = !w;
         if (!w) return false;
         const int r1 = (r0 + args.box - 1) & -args.box;
         uint8_t* p = sgen + (stage - sbase);
@@ -921,6 +923,7 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
         // let copies already issued land before the CTA's shared memory goes away
         volatile int never = 0;
         if (qn > 0) mbar_wait(bar(pbQFull), (qn - 1) & 1, &never, nullptr, kWaitLimitNs);
+        if (tail_out) mbar_wait(bar(pbTail), tails & 1, &never, nullptr, kWaitLimitNs);
         if constexpr (C::kPaired) {
           for (int i = max(0, pg - C::kSlots); i < pg; ++i)
             mbar_wait(bar(pbRingFull + i % C::kSlots), (i / C::kSlots) & 1, &never, nullptr,
