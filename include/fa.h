@@ -274,7 +274,10 @@ fa_status fa_read_paged(const void* k_pages, const void* v_pages, void* k_out, v
  *  a sequence's end does not matter, NaN included; a NaN or an infinity in a key or value of the
  *  sequence itself may reach any of its rows, those before that position too (a zero weight times it).
  *  workspace : >= fa_prefill_paged_workspace_bytes(Hq, Hkv, D) bytes on the current device, contents
- *              on entry irrelevant, not shared by calls in flight at the same time (see fa_fwd_ex) */
+ *              on entry irrelevant, not shared by calls in flight at the same time (see fa_fwd_ex).
+ *              After FA_ERR_TIMEOUT overwrite it (zeros will do) before a captured call is replayed
+ *              over it: until then replays whose units are cut report FA_ERR_TIMEOUT again, their
+ *              output incomplete.  Later uncaptured calls need nothing. */
 size_t fa_prefill_paged_workspace_bytes(int Hq, int Hkv, int D);
 fa_status fa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
                            const int32_t* block_table, const int32_t* row_starts,

@@ -112,7 +112,7 @@ struct PArgs {
   int G, tile_tok, box, box_bits;  // box = 1 << box_bits
   float scale_log2;
   float* part;       // partial rows of units cut between CTAs, 2 slots a CTA, 2 tiles a slot
-  uint32_t* pflags;  // [CTAs][2] publication flags, tagged per call
+  uint32_t* pflags;  // [CTAs][2] publication flags, tagged per call, then the tag of an abandoned call
   uint32_t tag;
 };
 
@@ -500,12 +500,23 @@ __device__ __forceinline__ uint32_t* flag_at(const PArgs& args, int c, int slot)
 __device__ __forceinline__ uint32_t* piece_flag(const PArgs& args, const PSeg& sg, int c) {
   return flag_at(args, c, sg.slot_first & -static_cast<int>(c == sg.c_first));
 }
+// A call that a CTA abandoned leaves flags set, which a replay of the same captured call (the same tag)
+// would take for its own: the CTA leaves the call's tag behind the flags, and until the workspace is
+// overwritten such a replay merges nothing and is reported as the abandoned call was.
+__device__ __forceinline__ uint32_t* abandoned_tag(const PArgs& args) {
+  return args.pflags + 2 * gridDim.x;
+}
 // whether all pieces but CTA `but`'s (-1: all pieces) are published, by one warp; their rows may be
 // read after it
 __device__ __forceinline__ bool pieces_there(const PArgs& args, const PSeg& sg, int but) {
+  const uint32_t gone = ld_relaxed_gpu(abandoned_tag(args));
   bool all = true;
   for (int c = sg.c_first + (threadIdx.x & 31); c <= sg.c_last; c += 32)
     all = all && (c == but || ld_relaxed_gpu(piece_flag(args, sg, c)) == args.tag);
+  if (gone == args.tag) {
+    atomicCAS(&g_prefill_paged_error, kErrNone, kErrTimeout);
+    all = false;
+  }
   all = __all_sync(0xffffffffu, all);
   if (all) {
     fence_acq_rel_gpu();  // each lane acquires the pieces whose flags it has read,
@@ -1414,9 +1425,12 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (threadIdx.x == 0 && *abort_flag) st_relaxed_gpu(abandoned_tag(args), args.tag);
 }
 
-size_t flag_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * sizeof(uint32_t); }
+size_t flag_bytes(int num_sms) {
+  return (static_cast<size_t>(num_sms) * 2 + 1) * sizeof(uint32_t);
+}
 
 template <int D, bool BF16, bool KQ4, bool VQ4>
 cudaError_t launch_t(const PagedPrefillLaunch& L, cudaStream_t stream) {
@@ -1457,7 +1471,7 @@ cudaError_t launch_fmt(const PagedPrefillLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-// publication flags, then the partial rows: two slots of two tiles for every CTA
+// publication flags and the word behind them, then the partial rows: two slots of two tiles for every CTA
 size_t paged_prefill_workspace(int D, int num_sms) {
   const size_t n = static_cast<size_t>(num_sms);
   return flag_bytes(num_sms) + 255 + n * 4 * (D + 2) * kBM * sizeof(float);
