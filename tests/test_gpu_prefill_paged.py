@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle
-from gpu_common import check_close, np64
+from gpu_common import UNIT_ROUNDOFF, check_close, np64
 from paged_common import DT, make_ragged, q4_buffer, q4_planes
 
 pytestmark = pytest.mark.gpu
@@ -510,3 +510,108 @@ def test_nan_in_a_key_reaches_every_row_that_sees_it(fa, kf, vf, dtype, D, at):
                 q4_planes(r.k, r.shape)[1][page, :, slot] = 0x7E00
         q = make_q(1, 4, D, dtype, seed=194)
         assert torch.isnan(run(fa, r, q)).all()
+
+
+RAMPS = [(n, kf, vf, dtype, D)
+         for n in (1, 5) for kf, vf in (("dense", "dense"), ("q4_0", "q4_0"), ("q4_0", "dense"))
+         for dtype in ("f16", "bf16") for D in (64, 128)]
+RAMPS += [(300, "dense", "dense", "bf16", 64), (300, "q4_0", "q4_0", "f16", 128),
+          (300, "dense", "q4_0", "bf16", 128), (300, "q4_0", "q4_0", "bf16", 64)]
+
+
+def check_ramp(r, q, o):
+    """Every element within the sum of the roundings' worst cases, for rows whose softmax rests on a few keys
+    (their outputs are as large as single values, for which check_close's absolute bar, stated for sums over
+    many keys, is too small: at |o| = 4 one rounding to bf16 alone is 4 * 2^-8 = 1.6e-2).  With u half a step
+    of the dtype, o = sum_j w_j v_j and A = sum_j w_j |v_j|:
+      o is rounded once                                     u |o|
+      P is rounded once, below 2^-14 by at most 2^-25       u A + n 2^-25 max|v|
+      a q4_0 value of V is rounded once                     u A
+      scores off by e move each w_j by a factor e at most
+      and their sum as well                                 e (A + |o|)
+    e is 2^-10 for the f32 accumulation (see the test) plus, for a q4_0 K, whose elements are rounded once,
+    scale u max_j sum_{i > 0} |q_i k_ji|.  (Element 0, the ramp, is exact: it is its block's largest, its
+    scale an eighth of it, and -8 times that the value again.)"""
+    u, scale = UNIT_ROUNDOFF[r.dtype], q.shape[-1] ** -0.5
+    for b, want in expected(r, q).items():
+        s, n, length = int(r.starts[b]), r.new[b], r.lens[b]
+        k, v = r.sequence("k", b), r.sequence("v", b)
+        qs = np64(q[s:s + n]).transpose(1, 0, 2)
+        size = oracle.attention(np.ascontiguousarray(qs[None]), k[None], np.ascontiguousarray(np.abs(v)[None]),
+                                causal=True, q_pos_offset=length - n, scale=scale)[0]
+        size, mag = size.transpose(1, 0, 2), np.abs(want)
+        e = np.full((n, qs.shape[0], 1), 2.0 ** -10)
+        if r.kf == "q4_0":
+            group = qs.shape[0] // k.shape[0]
+            for h in range(qs.shape[0]):
+                e[:, h, 0] += scale * u * (np.abs(qs[h, :, 1:]) @ np.abs(k[h // group, :, 1:]).T).max(-1)
+        bound = (u * (mag + size * (2 if r.vf == "q4_0" else 1)) + e * (size + mag)
+                 + length * 2.0 ** -25 * np.abs(v).max())
+        off = np.abs(np64(o[s:s + n]) - want)
+        assert (off <= bound).all(), (b, float((off / bound).max()))
+
+
+@pytest.mark.parametrize("step", [2.0, 12.0])
+@pytest.mark.parametrize("n,kf,vf,dtype,D", RAMPS)
+def test_frames_move_in_lone_tiles_and_pieces(fa, n, kf, vf, dtype, D, step):
+    """Scores that grow by `step` a key block, past the 10-point margin in every block or in every sixth, in
+    tiles alone in their unit (1 and 5 tokens) and in pairs, in units that stay whole (of up to 8 blocks) and
+    in pieces of several blocks, which are then merged with frames far apart.  The launches give the same
+    bytes.  (The largest score before scaling is below 2^13, so that its f32 accumulation over D / 16
+    products of 16, each rounded within 2^-23, moves a scaled score by less than 8 * 2^-10 / 8 = 2^-10 at
+    worst.)"""
+    Hkv, page = 8, 128
+    lens = [2500 + 37 * b for b in range(10 if n < 300 else 1)] + [900, 300 if n == 300 else 129]
+    r = make_ragged([n] * len(lens), lens, Hkv, D, page, dtype, "dense", vf, seed=211, poison=False)
+    for b, length in enumerate(lens):
+        for p in range(-(-length // page)):
+            r.k[int(r.table[b, p]), :, :, 0] = step * p / (8.0 * D ** -0.5)
+    if kf == "q4_0":
+        r.k, r.kf = q4_buffer(r.k), kf
+    q = make_q(sum(r.new), 4 * Hkv, D, dtype, seed=212)
+    q[..., 0] = 8.0
+    o = run(fa, r, q)
+    check_ramp(r, q, o.cpu())
+    args = (q.cuda(), r.pool(fa, "k"), r.pool(fa, "v"), *r.batch())
+    for _ in range(20):
+        assert torch.equal(o, fa.fa_prefill_paged(*args))
+    assert fa.fa_get_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("D,kf,vf", [(128, "dense", "dense"), (64, "q4_0", "q4_0"), (128, "dense", "q4_0"),
+                                     (128, "q4_0", "q4_0")])
+def test_merged_rows_at_other_strides(fa, D, kf, vf):
+    """Rows of cut units (two and many pieces) stored by the merges: o head-major, o with gaps between rows
+    and heads; what lies between stays as it was."""
+    new, Hq, Hkv, first, pad = [1, 600, 2, 77], 8, 2, 3, 6
+    lens = [9000, 4000, 3001, 1500]
+    n, rows = sum(new), first + sum(new) + pad
+    r = make_ragged(new, lens, Hkv, D, 64, "f16", kf, vf, seed=221, first_row=first)
+    fused = make_q(rows, Hq + 2 * Hkv, D, "f16", seed=222).cuda()
+    q = fused[:, :Hq]
+    k, v, batch = r.pool(fa, "k"), r.pool(fa, "v"), r.batch()
+    want = fa.fa_prefill_paged(q.contiguous(), k, v, *batch)
+    check(r, q.cpu(), want.cpu())
+    whole = torch.full((Hq, rows, D), 7.0, dtype=torch.float16, device="cuda")
+    gaps = torch.full((rows, Hq + 3, D + 8), 7.0, dtype=torch.float16, device="cuda")
+    for o in (whole.transpose(0, 1), gaps[:, 1:Hq + 1, :D]):
+        for _ in range(10):
+            o[first:first + n] = 0
+            fa.fa_prefill_paged(q, k, v, *batch, o)
+            assert torch.equal(o[first:first + n], want[first:first + n])
+        assert (o[:first] == 7.0).all() and (o[first + n:] == 7.0).all()
+    assert fa.fa_get_status() == fa.FA_OK
+    assert (gaps[:, 0] == 7.0).all() and (gaps[:, Hq + 1:] == 7.0).all() and (gaps[..., D:] == 7.0).all()
+
+
+@pytest.mark.parametrize("D,kf,vf", [(128, "dense", "dense"), (64, "dense", "q4_0"), (128, "q4_0", "q4_0"),
+                                     (64, "q4_0", "q4_0")])
+def test_cut_units_without_the_causal_mask(fa, D, kf, vf):
+    """All keys for every row: chunks and single tokens in many pieces, rows before the first key's position
+    among them."""
+    r = make_ragged([300, 1, 5, 40], [5000, 9000, 3, 1300], 2, D, 64, "f16", kf, vf, seed=231)
+    q = make_q(sum(r.new), 8, D, "f16", seed=232)
+    first = run(fa, r, q, causal=False)
+    check(r, q, first.cpu(), causal=False)
+    for _ in range(10):
+        assert torch.equal(first, run(fa, r, q, causal=False))
