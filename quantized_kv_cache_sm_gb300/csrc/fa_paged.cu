@@ -45,17 +45,11 @@ __device__ __forceinline__ bool locate_rows(const PagedBatch& b, int Hkv, int t0
   __shared__ int32_t s_lens[kSmemSeqs];
   const int tid = threadIdx.x;
   const bool small = b.B <= kSmemSeqs;
-  const bool reports = (blockIdx.x | blockIdx.y | blockIdx.z) == 0;  // bad lengths, of sequences
-                                                                     // without rows too
   const int64_t cap = static_cast<int64_t>(b.page_size) * b.pages_per_seq;
   int bad = 0;
   for (int i = tid; i < b.B; i += kThreads) {
     const int v = __ldg(b.starts + i), next = __ldg(b.starts + i + 1);
-    if (small || reports) {
-      const int len = __ldg(b.lens + i);
-      if (small) s_lens[i] = len;
-      if (reports && bad_length(len, cap)) atomicCAS(&g_paged_error, kErrNone, kErrBadIndex);
-    }
+    if (small) s_lens[i] = __ldg(b.lens + i);
     bad |= bad_start(v, next, b.rows);
     if (small) {
       s_starts[i] = v;
@@ -87,6 +81,10 @@ __device__ __forceinline__ bool locate_rows(const PagedBatch& b, int Hkv, int t0
       if (row < 0) atomicCAS(&g_paged_error, kErrNone, kErrBadIndex);
     }
     row_of[tid] = row;
+  } else if (tid >= kTok * kGroups && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) {
+    // meanwhile one CTA's other threads record bad lengths, of sequences without rows too
+    for (int i = tid - kTok * kGroups; i < b.B; i += kThreads - kTok * kGroups)
+      if (bad_length(lens[i], cap)) atomicCAS(&g_paged_error, kErrNone, kErrBadIndex);
   }
   __syncthreads();
   return true;
