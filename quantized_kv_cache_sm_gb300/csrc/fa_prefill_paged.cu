@@ -214,23 +214,16 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
 // P.  The first half's P stays packed in registers until the second half's scores are there and their
 // max shows, with the first half's row sum (see kSumTrigger), that no row of the warp needs the frame
 // test; from then on P goes over S as it is formed.  Otherwise -- a row's first block, a masked one, or
-// one that needs the test -- S is whole still and is read twice: for the block's max, and to form P in
-// the frame that follows.  Frames, P and sums are those of softmax_block to the bit.
+// one that needs the test -- S is whole still and is read twice, 32 keys at a time and no further than
+// some row sees: for the block's max, and to form P in the frame that follows.  Frames, P and sums are
+// those of softmax_block to the bit (a row that sees nothing of the block apart, whose are not used).
 //
 // (softmax_block's 128 scores in registers need 168 of them a thread, which sixteen warps have only
 // where the other warps hand theirs over.  Measured against that, us: 16 x 5 draft tokens over q4_0
-// 47.0 -> 45.8, five prompts with q4_0 V 19.0 -> 20.7, 2048 tokens at 16384 q4_0 keys 396 -> 416.  Other
-// forms within 128 registers on the same three: all of P kept until the row sum is known 46.9 / 19.6 /
-// 431, three quarters of it 45.5 / 20.8 / 422, a short form for masked blocks too 50.4 / 20.3 / 420, the
-// max first for every block 50.5 / 20.6 / 476.)
-template <bool MASK>
-__device__ __forceinline__ void mask_chunk(uint32_t (&r)[32], int c, int rel_lim) {
-  if (MASK) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (32 * c + i > rel_lim) r[i] = __float_as_uint(-INFINITY);
-  }
-}
+// 46.9 -> 42.3, 256 sequences of 64 q4_0 keys 74.0 -> 57.9, five prompts with q4_0 V 18.9 -> 20.4, 2048
+// tokens at 16384 q4_0 keys 396 -> 408.  The second way unrolled, over all 128 keys: 46.9 / 84.8 / 20.6 /
+// 410; all of P kept until the row sum is known 43.3 / 59.7 / 20.8 / 412, three quarters of it 42.5 /
+// 59.1 / 20.4 / 413.)
 __device__ __forceinline__ float max_chunk(const uint32_t (&r)[32]) {
   float m = -INFINITY;
 #pragma unroll
@@ -289,33 +282,44 @@ __device__ __forceinline__ bool exp_in_frame(uint32_t scol, float sl2, float f, 
   sum = row_sum(acc);
   return true;
 }
-template <bool MASK>
-__device__ __forceinline__ float block_max(uint32_t scol, int rel_lim) {
-  float m[4];
+// 32 keys' scores, those past lim set to -inf; false, and nothing loaded, where no row of the warp sees
+// any of them
+__device__ __forceinline__ bool seen_chunk(uint32_t scol, int lim, uint32_t (&r)[32]) {
+  if (__all_sync(0xffffffffu, lim < 0)) return false;
+  load_chunk(scol, 0, r);
+  tmem_wait_ld();
+  reg_fence32(r);
+  if (__any_sync(0xffffffffu, lim < 31)) {
 #pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i > lim) r[i] = __float_as_uint(-INFINITY);
+  }
+  return true;
+}
+__device__ __forceinline__ float block_max(uint32_t scol, int rel_lim) {
+  float m = -INFINITY;
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32];
-    load_chunk(scol, c, r);
-    tmem_wait_ld();
-    reg_fence32(r);
-    mask_chunk<MASK>(r, c, rel_lim);
-    m[c] = max_chunk(r);
+    if (!seen_chunk(scol + 32 * c, rel_lim - 32 * c, r)) break;
+    m = fmaxf(m, max_chunk(r));
   }
-  return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
+  return m;
 }
 // P in frame f over S, P of keys 32 c .. over S of keys 16 c .., which are read by then: the row sum
-template <bool MASK, bool BF16>
+template <bool BF16>
 __device__ __forceinline__ float exp_block(uint32_t scol, int rel_lim, float sl2, float f) {
   const uint64_t sl2x2 = f2_pack(sl2, sl2), nfx2 = f2_pack(-f, -f);
   RowSum acc = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t r[32], p[16];
-    load_chunk(scol, c, r);
-    tmem_wait_ld();
-    reg_fence32(r);
-    mask_chunk<MASK>(r, c, rel_lim);
-    exp_chunk<BF16>(r, p, sl2x2, nfx2, acc);
+    if (seen_chunk(scol + 32 * c, rel_lim - 32 * c, r)) {
+      exp_chunk<BF16>(r, p, sl2x2, nfx2, acc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[i] = 0u;
+    }
     tmem_st16(scol + 16 * c, p);
   }
   return row_sum(acc);
@@ -331,7 +335,7 @@ __device__ __forceinline__ void softmax_block_lean(uint32_t scol, uint32_t ocol,
       return;
     }
   }
-  const float m2 = (need_mask ? block_max<true>(scol, rel_lim) : block_max<false>(scol, rel_lim)) * sl2;
+  const float m2 = block_max(scol, rel_lim) * sl2;
   const bool need = m2 > f + kMarginLog2;
   float alpha = 1.f;
   if (need) {
@@ -352,8 +356,7 @@ __device__ __forceinline__ void softmax_block_lean(uint32_t scol, uint32_t ocol,
       tmem_st32(ocol + 32 * c, r);
     }
   }
-  l += need_mask ? exp_block<true, BF16>(scol, rel_lim, sl2, f)
-                 : exp_block<false, BF16>(scol, rel_lim, sl2, f);
+  l += exp_block<BF16>(scol, rel_lim, sl2, f);
 }
 
 // Merge of one unit's pieces by the 256 softmax threads.  A tile's threads (both tiles' where tile
