@@ -13,8 +13,9 @@
 //
 // Measured (one GB300, 8 kv heads, D = 128, K and V): 4 x 16384 rows read out of f16 pools 82 us (6.5
 // TB/s), out of q4_0 pools 56 us (6.1 TB/s); 4 x 2048 bf16 rows appended to q4_0 pools and read back
-// 24 us; 64 rows appended and read back 5.6 us.  With 16 bytes of the dense row a thread, integer
-// conversions and run-time divisions in the loop the same took 86, 87, 31 and 11 us.
+// 25 us, the append alone 15.4, into dense pools 14.7; 64 rows appended and read back 6.0 us.  With 16
+// bytes of the dense row a thread, integer conversions and run-time divisions in the loop the first
+// three and the last took 86, 87, 31 and 11 us.
 #include <algorithm>
 
 #include "fa_internal.h"

@@ -86,7 +86,8 @@ struct PagedPlan {
   // A cut costs its pieces' round trip through memory and their merge: units of up to so many blocks
   // stay whole (a run's end inside one moves to the nearer end of it), longer ones are cut anywhere.
   // Measured, D = 64, f16 K and q4_0 V, prompts of up to 1000 tokens: 19.2 us with 8 or 16, 20.8
-  // with 0 or 4; 16 sequences of mixed lengths, bf16 at D = 128: 52.5 us with 0 or 8, 67.0 with 16.
+  // with 0 or 4; 16 sequences of mixed lengths, bf16 at D = 128: 52.5 us with 0 or 8, 67.0 with 16
+  // (these before later steps took the calls themselves to other times).
   // A limit of 32 for units of one 32-row quarter of a tile alone took 16 sequences of a few q4_0
   // draft tokens from 48.0 to 45.8 us, and the mixed batch from 52.5 to 58.5.
   static constexpr int kWhole = 8;

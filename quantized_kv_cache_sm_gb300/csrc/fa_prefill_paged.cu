@@ -28,14 +28,14 @@
 //
 // What bounds it, measured on one GB300 (GQA 32/8, D = 128; us a call from a CUDA graph): long chunks
 // by each tile's softmax and hand-offs behind the other tile's MMAs, 2048 tokens at the end of 16384
-// f16 keys 328 (1570 TFLOP/s, tensor pipe active 66 %), over q4_0 pools 392, where the dequant takes
+// f16 keys 330 (1560 TFLOP/s, tensor pipe active 66 %), over q4_0 pools 407, where the dequant takes
 // issue slots and shared-memory bandwidth; single tokens over dense pools by HBM, 64 sequences of
-// 8192 bf16 keys 333 (6.4 TB/s); over q4_0 pools by the lone tile's block step (dequant and operand
-// reads in shared memory, 1.3 us with f16, 1.5 with bf16), the same batch 339; small calls by the 13
-// us of launch, plan, first loads and merges.
+// 8192 bf16 keys 330 (6.5 TB/s); over q4_0 pools by the lone tile's block step (dequant and operand
+// reads in shared memory, 1.2 us with f16, 1.5 with bf16), the same batch 271 and 335; small calls by
+// the 13 us of launch, plan, first loads and merges.
 //
 // Warp roles: as in fa_prefill.cu (0 producer and scheduler, 1 TMEM and MMA issuer, 2-3 and 12-15
-// q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B).
+// q4_0 dequant, 4-7 softmax of tile A, 8-11 of tile B), without moving registers between them.
 #include <limits.h>
 #include <stddef.h>
 
@@ -1193,11 +1193,11 @@ __global__ void __launch_bounds__(Cfg<D, KQ4, VQ4, true>::kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax rows
-    // Registers: a block's 128 scores and little else.  Nothing but the two words below is carried
-    // from one segment to the next, and what follows from the thread's number or the segment is
-    // formed again where it is used: values kept across the block loop, or across the call that
-    // ends a cut segment, would be spilled inside it (measured: 343 -> 383 us on the 2048-token
-    // chunk at 16384 keys).
+    // Registers: a block's 128 scores (with a q4_0 side 64, and 64 as P) and little else.  Nothing but
+    // the two words below is carried from one segment to the next, and what follows from the thread's
+    // number or the segment is formed again where it is used: values kept across the block loop, or
+    // across the call that ends a cut segment, would be spilled inside it (measured: 343 -> 383 us on
+    // the 2048-token chunk at 16384 f16 keys).
     enum : uint32_t {
       kPhS = 1,       // barrier phases: S-full,
       kPhAlt = 2,     // S-full of the second buffer,

@@ -52,7 +52,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + alignment slack
   // warps: 0 producer, 1 MMA issuer, 4-11 softmax (one thread per query row), 2-3 dequant
   // with q4_0 K or V; WIDE adds dequant warps 12-15 (sixteen warps, 128 registers a thread at
-  // launch; the kernels then move registers from warpgroups 0 and 3 to the two softmax
+  // launch; fa_prefill.cu then moves registers from warpgroups 0 and 3 to the two softmax
   // warpgroups, 88 and 168 a thread).  Measured at 16K keys, q4_0 K and V: with two dequant
   // warps the step waits for dequantized tiles; six of them took the cut kernel from 0.477 to
   // 0.410 ms and the one-unit kernel from 0.484 to 0.443 ms.
@@ -200,9 +200,9 @@ constexpr float kSumTrigger = 21800.f;
 // its row sum to l.  O may be rescaled in place: S(j) being ready means PV(j-1) has completed
 // (QK(j) was issued after it).  The caller waits for the TMEM stores.
 //
-// One TMEM wait per block: the 128 scores stay in registers (168 a thread in every layout;
-// with q4_0 sides by a register split between warpgroups) and P is formed in the current frame
-// first.
+// One TMEM wait per block: the 128 scores stay in registers (168 a thread; in fa_prefill.cu's
+// layouts with q4_0 sides by a register split between warpgroups) and P is formed in the current
+// frame first.
 //
 // pmx tracks a bound on the largest P written (before its rounding to the dtype), each in the
 // frame in force for its block: the exact largest P of a block that ran the frame test (P is
