@@ -757,6 +757,9 @@ def fa_prefill_paged(q: torch.Tensor, k_pages, v_pages, block_table: torch.Tenso
             o = torch.zeros((rows, Hq, D), dtype=dtype, device=q.device)
     qp, qrs, qhs = _packed(q, "q", dtype, Hq, D, rows)
     op, ors, ohs = _packed(o, "o", dtype, Hq, D, rows)
+    if workspace is not None and not workspace.is_contiguous():
+        # (its size is taken from its number of elements, which an expanded tensor does not hold)
+        raise ValueError("workspace must be contiguous")
     device = _here(q, kt, vt, o, block_table, row_starts, seq_lens, workspace)
     lib = load()
     if workspace is None:

@@ -104,3 +104,13 @@ def test_binding_refusals():
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+def test_workspace_that_does_not_hold_its_elements_is_refused():
+    """An expanded tensor has as many elements as asked for and memory for one."""
+    h, i32 = torch.float16, dict(dtype=torch.int32)
+    q, pool = torch.zeros(5, 8, 128, dtype=h), torch.zeros(4, 2, 16, 128, dtype=h)
+    batch = (torch.zeros(2, 3, **i32), torch.zeros(3, **i32), torch.zeros(2, **i32))
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 40)
+    with pytest.raises(ValueError, match="contiguous"):
+        fa.fa_prefill_paged(q, pool, pool, *batch, workspace=ws)
