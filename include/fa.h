@@ -221,7 +221,8 @@ fa_status fa_decode_paged(const void* q, const void* k_pages, const void* v_page
  *                elements, multiples of 8 and not negative (a tensor cut out of a fused projection,
  *                or head-major rows, need no copy).  Every base pointer 16-byte aligned.  No two
  *                (row, head) of a tensor overlap (new keys and values, which are only read, may:
- *                a stride of 0 broadcasts).
+ *                a stride of 0 broadcasts), and what a call writes overlaps nothing else that it
+ *                reads or writes.
  *  row_starts  : device int32 [B + 1]: sequence b owns rows row_starts[b] .. row_starts[b + 1] - 1,
  *                n_b >= 0 of them.  Rising from row_starts[0] >= 0 to row_starts[B] <= rows; rows
  *                outside (padding up to a fixed batch size) are not written, and what they hold does
